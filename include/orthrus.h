@@ -407,6 +407,168 @@ orthrus_status orthrus_linear(const void* X, const void* W, float* Y, int32_t M,
 orthrus_status orthrus_linear_noalloc(const void* X, const void* W, float* Y, int32_t M, int32_t N, int32_t Kd,
                                       int32_t* status, orthrus_stream stream);
 
+/* ---- draft trees -----------------------------------------------------------
+ * One verify forward can check many drafts at once when they form a tree: node 0
+ * is the pending token, and every other node continues its parent. Nodes share
+ * the prefix on the way to the root, so a node sits at position len + depth and
+ * sees the cache, itself and its ancestors. The tree's K/V stay in a scratch of
+ * their own; only the accepted path's rows enter the cache.
+ *   parents  device int32 [batch][nodes]: parents[b][i] < i is node i's parent, -1 a
+ *            root (parents[b][0] = -1);
+ *   n_nodes  device int32 [batch], nullable (all `nodes`): nodes at or past
+ *            n_nodes[b] are padding and their entries are not read; 0 = an idle
+ *            sequence.
+ * 1 <= nodes <= ORTHRUS_TREE_MAX_NODES, 1 <= batch <= ORTHRUS_TREE_MAX_BATCH. These calls need no
+ * plan, keep no state between calls and allocate nothing. */
+#define ORTHRUS_TREE_MAX_NODES 256
+#define ORTHRUS_TREE_MAX_BATCH 1024
+
+/* Element types of the operators below. ORTHRUS_BF16_PLANES is an output type: two bf16 planes, hi = bf16(x)
+ * and then lo = bf16(x - hi), as the projections of this library read them. */
+enum { ORTHRUS_FP32 = 0, ORTHRUS_BF16 = 1, ORTHRUS_FP16 = 2, ORTHRUS_BF16_PLANES = 3 };
+
+/* Depths and visibility words of a batch of trees. depth: int32 [batch][nodes], the
+ * number of edges to the root; mask: uint64 [batch][nodes][(nodes + 63) / 64], bit
+ * j % 64 of word j / 64 set iff node i sees node j (itself and its ancestors).
+ * Padding nodes get depth 0 and no bits. A parent outside [-1, i) sets the device
+ * status ORTHRUS_ERR_ARG (nullable) and counts as a root, and so does an n_nodes[b]
+ * outside [0, nodes], which is clamped. Errors: ORTHRUS_ERR_ARG. */
+orthrus_status orthrus_tree_layout(const int32_t* parents, const int32_t* n_nodes, int32_t batch, int32_t nodes,
+                                   int32_t* depth, uint64_t* mask, int32_t* status, orthrus_stream stream);
+
+/* Attention of a draft tree for one layer's cache:
+ *   q        [batch][Hkv][nodes*G][d]: row i*G + g is query head kvh*G+g at node i;
+ *   k_cache, v_cache  [batch][Hkv][capacity][d]: rows [0, len[b]) are seen by every node;
+ *   k_blk, v_blk      [batch][Hkv][blk_stride][d], blk_stride >= nodes: the tree's own
+ *            K/V, row j seen by node i iff its bit is set in mask (any visibility is
+ *            allowed, also none; bits at or past n_nodes[b] count as unset);
+ *   type     of q, K and V: ORTHRUS_FP16 (this library's caches) or ORTHRUS_BF16;
+ *   scale    of the scores; 0 = 1 / sqrt(d);
+ *   out      [batch*nodes][H*d] of out_type ORTHRUS_FP16 or ORTHRUS_BF16, or
+ *            ORTHRUS_BF16_PLANES [2][batch*nodes][H*d] (token-major, head h at columns h*d..).
+ * Rows of padding nodes are left as they were. A row that sees nothing (an empty
+ * cache and no bits) is zero. Rows that no node sees may hold anything, NaN included.
+ * A len[b] outside [0, capacity] sets the status and is clamped. Softmax statistics and sums are fp32; the
+ * softmax weights are rounded to `type` for their product with V.
+ * 1 <= G <= 32, d in {64, 128}; q, K, V and out 16-byte aligned, mask 8-byte. The scratch
+ * (orthrus_tree_attention_workspace_bytes, at most 64 MiB, 256-byte aligned) needs no initialisation and is
+ * free again when the call's kernels are done; calls that may overlap on the GPU
+ * need one each. Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_UNSUPPORTED, ORTHRUS_ERR_WORKSPACE, ORTHRUS_ERR_CUDA. */
+size_t orthrus_tree_attention_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t group, int32_t nodes,
+                                              int32_t head_dim);
+orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const void* v_cache, const void* k_blk,
+                                      const void* v_blk, const int32_t* len, const int32_t* n_nodes,
+                                      const uint64_t* mask, int32_t batch, int32_t n_kv_heads, int32_t group,
+                                      int32_t nodes, int32_t head_dim, int32_t capacity, int32_t blk_stride,
+                                      int32_t type, int32_t out_type, float scale, void* out, void* workspace,
+                                      size_t workspace_bytes, int32_t* status, orthrus_stream stream);
+
+/* Greedy consensus on a tree, and the accepted path's K/V into the cache. tokens and
+ * argmax: int32 [batch][nodes], the token at each node (tokens[b][0], the pending token, is
+ * not read) and the verifier's argmax there. From node 0 the walk steps to the
+ * lowest-indexed child whose token is the argmax at the current node, until there
+ * is none; a = its number of steps. Outputs (device int32):
+ *   path [batch][nodes]       the walk's nodes, 0 first, then -1;
+ *   committed [batch][nodes]  the a accepted tokens, then the argmax at the walk's end, then -1;
+ *   accept_len[b] = a;  pending[b] = the argmax at the walk's end;
+ *   new_len[b] = len[b] + a + 1 (may be the same array as len).
+ * In every layer and KV head, scratch row path[j] of k_blk and v_blk
+ * ([n_layers][batch][Hkv][blk_stride][d]) is copied to cache row len[b] + j
+ * ([n_layers][batch][Hkv][capacity][d]), j = 0..a; the buffers must not overlap. Elements are
+ * 16 bits wide, d a multiple of 8, the four buffers 16-byte aligned. A sequence without
+ * room (len + a + 1 > capacity: status ORTHRUS_ERR_CAPACITY), an idle one (n_nodes[b] = 0), or any
+ * while the status word holds an error commits nothing: accept_len = -1, path and committed all -1,
+ * pending and the cache unchanged, new_len = len. Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_UNSUPPORTED, ORTHRUS_ERR_CUDA. */
+orthrus_status orthrus_tree_commit(const int32_t* parents, const int32_t* tokens, const int32_t* argmax,
+                                   const int32_t* n_nodes, const void* k_blk, const void* v_blk, int32_t blk_stride,
+                                   void* k_cache, void* v_cache, int32_t n_layers, int32_t batch, int32_t n_kv_heads,
+                                   int32_t capacity, int32_t head_dim, int32_t nodes, const int32_t* len,
+                                   int32_t* new_len, int32_t* pending, int32_t* accept_len, int32_t* path,
+                                   int32_t* committed, int32_t* status, orthrus_stream stream);
+
+/* Verify view over a draft tree, with a plan: one forward of the frozen model over
+ * [pending, tokens[b][1..nodes)] at positions len + depth, every node seeing the cache,
+ * itself and its ancestors. tokens, parents, n_nodes as above; nodes <= max_block. Writes argmax (device int32 [batch][nodes])
+ * and leaves the tree's base K/V in the block scratch, which the next draft or tree
+ * view overwrites; cache and len are not changed. logits (nullable): fp32
+ * [batch][nodes][vocab]. Entries of padding nodes are unspecified. A tree that is a chain gives
+ * what orthrus_verify_block gives, up to rounding. Errors: ORTHRUS_ERR_ARG; device status as
+ * orthrus_verify_block and orthrus_tree_layout. */
+orthrus_status orthrus_verify_tree(const void* plan, const int32_t* pending, const int32_t* tokens,
+                                   const int32_t* parents, const int32_t* n_nodes, int32_t nodes, int32_t* argmax,
+                                   float* logits, orthrus_stream stream);
+
+/* orthrus_tree_commit on the plan's cache and block scratch, after orthrus_verify_tree:
+ * cache.len and pending advance in place. */
+orthrus_status orthrus_accept_commit_tree(const void* plan, int32_t* pending, const int32_t* tokens,
+                                          const int32_t* parents, const int32_t* n_nodes, const int32_t* argmax,
+                                          int32_t nodes, int32_t* accept_len, int32_t* path, int32_t* committed,
+                                          orthrus_stream stream);
+
+/* ---- rotary positions --------------------------------------------------- */
+
+/* Frequencies of a rotary embedding: pair p turns by turns[p] full turns per position. Filled by
+ * orthrus_rope_init; a caller with frequencies of its own may fill it directly. */
+typedef struct {
+  int32_t head_dim, rot_dim; /* dims [0, rot_dim) of a head are rotated, the others copied */
+  int32_t interleaved;       /* pairs (2p, 2p + 1) if set, else (p, p + rot_dim / 2) */
+  float gain;                /* factor on the rotated dims */
+  double turns[128];         /* [rot_dim / 2] */
+} orthrus_rope;
+
+/* How frequencies are changed for contexts longer than the trained one (`factor` times
+ * `original` positions); f_p = theta^(-2p / rot_dim) is the plain frequency:
+ *   NONE      f_p;
+ *   LINEAR    f_p / factor;
+ *   BY_PARTS  f_p (k + (1 - k) / factor), k = clamp((r_p - slow) / (fast - slow), 0, 1),
+ *             r_p = original f_p / 2 pi the pair's rotations over the original context;
+ *   BY_INDEX  the same with k = 1 - clamp((p - lo) / (hi - lo), 0, 1), lo and hi the whole
+ *             indexes at or outside those whose r is `fast` and `slow` (lo >= 0, hi <= rot_dim - 1;
+ *             hi - lo at least 0.001).
+ * gain 0 = 1 for NONE and LINEAR, 0.1 ln(factor) + 1 for the others ("YaRN", Peng et
+ * al. 2023, section 3.4; BY_PARTS is its NTK-by-parts formula). */
+enum { ORTHRUS_ROPE_NONE = 0, ORTHRUS_ROPE_LINEAR = 1, ORTHRUS_ROPE_BY_PARTS = 2, ORTHRUS_ROPE_BY_INDEX = 3 };
+
+/* Fill *rope on the host (no GPU). head_dim and rot_dim even, 2 <= rot_dim <= head_dim <= 256; theta > 1;
+ * factor >= 1, original >= 1 and 0 < slow < fast where the scaling uses them; gain >= 0. ORTHRUS_ERR_ARG otherwise. */
+orthrus_status orthrus_rope_init(orthrus_rope* rope, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                 float theta, int32_t scaling, float factor, int32_t original, float slow, float fast,
+                                 float gain);
+
+/* One tensor of an orthrus_rotary call: value (b, t, h, e) is read at
+ *   src[b src_batch + t src_token + h src_head + e]     (strides in elements)
+ * and written at
+ *   dst[b dst_batch + row dst_token + (h / group) dst_kv + (h % group) dst_head + e],
+ * row = t, or len[b] + t with ORTHRUS_ROTARY_APPEND (only rows in [0, rows) are
+ * written; others set the status ORTHRUS_ERR_CAPACITY). group = 1 for plain heads; G with
+ * dst_kv = nodes*G*d, dst_token = G*d, dst_head = d is the attention's q layout. */
+typedef struct {
+  const void* src;
+  void* dst; /* the same memory as src (same type and strides), or memory that overlaps no source */
+  int32_t src_type, dst_type; /* ORTHRUS_FP32, ORTHRUS_BF16 or ORTHRUS_FP16 */
+  int32_t heads, group, flags, rows;
+  int64_t src_batch, src_token, src_head;
+  int64_t dst_batch, dst_token, dst_kv, dst_head;
+} orthrus_rotary_part;
+
+enum {
+  ORTHRUS_ROTARY_MAX_PARTS = 3,
+  ORTHRUS_ROTARY_COPY = 1,       /* no rotation (V beside q and k) */
+  ORTHRUS_ROTARY_APPEND = 2,     /* destination row len[b] + t */
+  ORTHRUS_ROTARY_BF16_VALUES = 4 /* round to bf16 before the conversion to dst_type (the cache's precision) */
+};
+
+/* Turn the heads of up to three tensors (q, k, and v copied) at positions
+ * len[b] + offsets[b][t], in one launch. len (device int32 [batch], nullable: 0) and offsets
+ * (device int32 [batch][tokens], nullable: t; a tree's depths). inverse != 0 turns back by the same
+ * angles with the same gain: the gradient with respect to the heads. Angles are
+ * formed in fp64, the rotation in fp32. Any strides and element-aligned pointers are
+ * taken; 16-byte accesses are used where they allow it. batch or tokens 0 is nothing to
+ * do. Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_CUDA. */
+orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_part* parts, int32_t n_parts,
+                              int32_t batch, int32_t tokens, const int32_t* len, const int32_t* offsets,
+                              int32_t inverse, int32_t* status, orthrus_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,15 +5,18 @@
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC_DIR = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "liborthrus.so")
-MAIN = os.path.join(SRC_DIR, "orthrus.cu")
+OBJ_DIR = os.path.join(HERE, "_build")  # object files, one per translation unit
+UNITS = [os.path.join(SRC_DIR, u) for u in ("orthrus.cu", "operators.cu")]
 
 
 def _nvcc() -> str:
@@ -38,18 +41,50 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17", "-shared",
-           "-Xcompiler", "-fPIC", "-I", INCLUDE, "-o", LIB + ".tmp", MAIN]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
+def _includes(path: str, seen: set) -> set:
+    """`path` and the project files it includes, directly or not."""
+    if path in seen:
+        return seen
+    seen.add(path)
+    with open(path) as f:
+        for name in re.findall(r'^\s*#include "([^"]+)"', f.read(), flags=re.M):
+            for d in (SRC_DIR, INCLUDE):
+                if os.path.exists(os.path.join(d, name)):
+                    _includes(os.path.join(d, name), seen)
+    return seen
+
+
+def _run(cmd, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     if verbose:
         sys.stderr.write(r.stderr)
+
+
+def _compile(src: str, force: bool, verbose: bool) -> str:
+    """Object file of one translation unit; compiled when one of its files is newer."""
+    obj = os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
+    if not force and os.path.exists(obj) and all(os.path.getmtime(f) <= os.path.getmtime(obj)
+                                                 for f in _includes(src, set())):
+        return obj
+    cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+           "-Xcompiler", "-fPIC", "-I", INCLUDE, "-c", "-o", obj + ".tmp", src]
+    if verbose:
+        cmd.insert(1, "-Xptxas=-v")
+    _run(cmd, verbose)
+    os.replace(obj + ".tmp", obj)
+    return obj
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with ThreadPoolExecutor(len(UNITS)) as pool:
+        objs = list(pool.map(lambda u: _compile(u, force, verbose), UNITS))
+    _run([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp"]
+         + objs, verbose)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

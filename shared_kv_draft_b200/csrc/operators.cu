@@ -1,0 +1,269 @@
+// Draft trees and rotary positions: launch geometry and the C-ABI entry points that need
+// no plan (declared in include/orthrus.h).
+#include "host.cuh"
+#include "operators.cuh"
+#include "orthrus.h"
+#include "rotary.cuh"
+#include "tree.cuh"
+#include "tree_attention.cuh"
+
+using namespace orthrus;
+
+bool orthrus::tree_sizes_ok(int batch, int nodes) {
+  return batch >= 1 && batch <= ORTHRUS_TREE_MAX_BATCH && nodes >= 1 && nodes <= ORTHRUS_TREE_MAX_NODES;
+}
+
+size_t orthrus::tree_attn_scratch(int B, int Hkv, int G, int nodes, int d) {
+  (void)B, (void)Hkv, (void)G, (void)nodes, (void)d;
+  return 256;
+}
+
+orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& a, void* workspace, cudaStream_t st) {
+  (void)workspace;
+  const long long rows = (long long)a.B * a.Hkv * a.N * a.G;
+  const dim3 grid((unsigned)((rows + 3) / 4));
+  const cudaError_t e = a.d == 128 ? launch(tree_attention_kernel<128>, grid, dim3(128), 0, st, a)
+                                   : launch(tree_attention_kernel<64>, grid, dim3(128), 0, st, a);
+  return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
+}
+
+orthrus_status orthrus::launch_tree_layout(const int* parents, const int* n_nodes, int batch, int nodes, int* depth,
+                                  unsigned long long* mask, int* status, cudaStream_t st) {
+  const cudaError_t e = launch(tree_layout_kernel, dim3(batch), dim3(round_up(nodes, 32)), 0, st, parents, n_nodes,
+                               nodes, (nodes + 63) / 64, depth, mask, status);
+  return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
+}
+
+orthrus_status orthrus::launch_tree_embed(const TreeEmbedArgs& a, int rows, cudaStream_t st) {
+  return launch(tree_embed_kernel, dim3(rows), dim3(256), 0, st, a) == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
+}
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+orthrus_status launch_tree_commit(const TreeWalkArgs& w, TreeMoveArgs m, int n_layers, int head_dim, cudaStream_t st) {
+  m.accept_len = w.accept_len;
+  m.new_len = w.new_len;
+  m.path = w.path;
+  m.batch = w.batch;
+  m.nodes = w.nodes;
+  m.capacity = w.capacity;
+  m.pieces = head_dim / 8;
+  const int warps = std::min(kWalkThreads / 32, w.batch);
+  if (launch(tree_walk_kernel, dim3(1), dim3(32 * warps), 0, st, w) != cudaSuccess) return ORTHRUS_ERR_CUDA;
+  if (launch(tree_move_kernel, dim3((unsigned)((size_t)n_layers * m.batch * m.kv_heads)), dim3(kMoveThreads), 0, st,
+             m) != cudaSuccess)
+    return ORTHRUS_ERR_CUDA;
+  return ORTHRUS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+orthrus_status orthrus_tree_layout(const int32_t* parents, const int32_t* n_nodes, int32_t batch, int32_t nodes,
+                                   int32_t* depth, uint64_t* mask, int32_t* status, orthrus_stream stream) {
+  if (!parents || !depth || !mask || !tree_sizes_ok(batch, nodes) || !aligned(mask, 8)) return ORTHRUS_ERR_ARG;
+  return launch_tree_layout(parents, n_nodes, batch, nodes, depth, (unsigned long long*)mask, status,
+                            (cudaStream_t)stream);
+}
+
+size_t orthrus_tree_attention_workspace_bytes(int32_t batch, int32_t n_kv_heads, int32_t group, int32_t nodes,
+                                              int32_t head_dim) {
+  if (!tree_sizes_ok(batch, nodes) || n_kv_heads < 1 || group < 1 || group > 32 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return tree_attn_scratch(batch, n_kv_heads, group, nodes, head_dim);
+}
+
+orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const void* v_cache, const void* k_blk,
+                                      const void* v_blk, const int32_t* len, const int32_t* n_nodes,
+                                      const uint64_t* mask, int32_t batch, int32_t n_kv_heads, int32_t group,
+                                      int32_t nodes, int32_t head_dim, int32_t capacity, int32_t blk_stride,
+                                      int32_t type, int32_t out_type, float scale, void* out, void* workspace,
+                                      size_t workspace_bytes, int32_t* status, orthrus_stream stream) {
+  if (!q || !k_cache || !v_cache || !k_blk || !v_blk || !len || !mask || !out || !workspace) return ORTHRUS_ERR_ARG;
+  if (!tree_sizes_ok(batch, nodes) || n_kv_heads < 1 || group < 1 || capacity < 1 || blk_stride < nodes)
+    return ORTHRUS_ERR_ARG;
+  if (!(scale >= 0.f) || scale == INFINITY) return ORTHRUS_ERR_ARG;
+  if (type != ORTHRUS_FP16 && type != ORTHRUS_BF16) return ORTHRUS_ERR_ARG;
+  if (out_type != ORTHRUS_FP16 && out_type != ORTHRUS_BF16 && out_type != ORTHRUS_BF16_PLANES) return ORTHRUS_ERR_ARG;
+  if (group > 32 || (head_dim != 64 && head_dim != 128)) return ORTHRUS_ERR_UNSUPPORTED;
+  if ((long long)batch * n_kv_heads > (1 << 20)) return ORTHRUS_ERR_UNSUPPORTED;
+  for (const void* p : {q, k_cache, v_cache, k_blk, v_blk, (const void*)out})
+    if (!aligned(p, 16)) return ORTHRUS_ERR_ARG;
+  if (!aligned(mask, 8) || !aligned(workspace, 256)) return ORTHRUS_ERR_ARG;
+  if (workspace_bytes < tree_attn_scratch(batch, n_kv_heads, group, nodes, head_dim)) return ORTHRUS_ERR_WORKSPACE;
+  TreeAttnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_blk = k_blk;
+  a.v_blk = v_blk;
+  a.len = len;
+  a.n_nodes = n_nodes;
+  a.mask = (const unsigned long long*)mask;
+  a.B = batch;
+  a.Hkv = n_kv_heads;
+  a.G = group;
+  a.N = nodes;
+  a.d = head_dim;
+  a.cap = capacity;
+  a.blk_stride = blk_stride;
+  a.words = (nodes + 63) / 64;
+  a.bf16 = type == ORTHRUS_BF16;
+  a.out_type = out_type;
+  a.scale_log2 = (float)(1.4426950408889634 * (scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_dim)));
+  a.out = out;
+  a.out_lo = (size_t)batch * nodes * n_kv_heads * group * head_dim;
+  a.status = status;
+  return launch_tree_attention(a, workspace, (cudaStream_t)stream);
+}
+
+orthrus_status orthrus_tree_commit(const int32_t* parents, const int32_t* tokens, const int32_t* argmax,
+                                   const int32_t* n_nodes, const void* k_blk, const void* v_blk, int32_t blk_stride,
+                                   void* k_cache, void* v_cache, int32_t n_layers, int32_t batch, int32_t n_kv_heads,
+                                   int32_t capacity, int32_t head_dim, int32_t nodes, const int32_t* len,
+                                   int32_t* new_len, int32_t* pending, int32_t* accept_len, int32_t* path,
+                                   int32_t* committed, int32_t* status, orthrus_stream stream) {
+  if (!parents || !tokens || !argmax || !k_blk || !v_blk || !k_cache || !v_cache || !len || !new_len || !pending ||
+      !accept_len || !path || !committed)
+    return ORTHRUS_ERR_ARG;
+  if (!tree_sizes_ok(batch, nodes) || blk_stride < nodes || n_layers < 1 || n_kv_heads < 1 || capacity < 1 ||
+      head_dim < 1)
+    return ORTHRUS_ERR_ARG;
+  if (head_dim % 8 || head_dim > 1024 || (long long)n_layers * batch * n_kv_heads > INT32_MAX)
+    return ORTHRUS_ERR_UNSUPPORTED;
+  for (const void* p : {k_blk, v_blk, (const void*)k_cache, (const void*)v_cache})
+    if (!aligned(p, 16)) return ORTHRUS_ERR_ARG;
+  TreeWalkArgs w;
+  w.parents = parents;
+  w.tokens = tokens;
+  w.argmax = argmax;
+  w.n_nodes = n_nodes;
+  w.batch = batch;
+  w.nodes = nodes;
+  w.capacity = capacity;
+  w.len = len;
+  w.new_len = new_len;
+  w.pending = pending;
+  w.accept_len = accept_len;
+  w.path = path;
+  w.committed = committed;
+  w.status = status;
+  TreeMoveArgs m;
+  m.k_blk = (const uint4*)k_blk;
+  m.v_blk = (const uint4*)v_blk;
+  m.k_cache = (uint4*)k_cache;
+  m.v_cache = (uint4*)v_cache;
+  m.kv_heads = n_kv_heads;
+  m.blk_stride = blk_stride;
+  return launch_tree_commit(w, m, n_layers, head_dim, (cudaStream_t)stream);
+}
+
+orthrus_status orthrus_rope_init(orthrus_rope* rope, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                 float theta, int32_t scaling, float factor, int32_t original, float slow, float fast,
+                                 float gain) {
+  if (!rope || head_dim < 2 || head_dim > 2 * kRotaryMaxPairs || head_dim % 2 || rot_dim < 2 || rot_dim > head_dim ||
+      rot_dim % 2)
+    return ORTHRUS_ERR_ARG;
+  if (!(theta > 1.f && theta < INFINITY) || !(gain >= 0.f && gain < INFINITY) || scaling < ORTHRUS_ROPE_NONE ||
+      scaling > ORTHRUS_ROPE_BY_INDEX)
+    return ORTHRUS_ERR_ARG;
+  if (scaling != ORTHRUS_ROPE_NONE && !(factor >= 1.f && factor < INFINITY)) return ORTHRUS_ERR_ARG;
+  const bool ramp = scaling == ORTHRUS_ROPE_BY_PARTS || scaling == ORTHRUS_ROPE_BY_INDEX;
+  if (ramp && (original < 1 || !(slow > 0.f) || !(fast > slow) || !(fast < INFINITY))) return ORTHRUS_ERR_ARG;
+  const double two_pi = 6.283185307179586476925;
+  const double th = (double)theta, k = (double)factor;
+  memset(rope, 0, sizeof(*rope));
+  rope->head_dim = head_dim;
+  rope->rot_dim = rot_dim;
+  rope->interleaved = interleaved != 0;
+  rope->gain = gain > 0.f ? gain : (ramp ? (float)(0.1 * std::log(k) + 1.0) : 1.f);
+  double lo = 0, hi = 0;
+  if (scaling == ORTHRUS_ROPE_BY_INDEX) {
+    auto index = [&](double rotations) {
+      return rot_dim * std::log(original / (two_pi * rotations)) / (2.0 * std::log(th));
+    };
+    lo = std::max(std::floor(index((double)fast)), 0.0);
+    hi = std::min(std::ceil(index((double)slow)), (double)(rot_dim - 1));
+    hi = std::max(hi, lo + 1e-3);
+  }
+  for (int p = 0; p < rot_dim / 2; ++p) {
+    double f = std::pow(th, -2.0 * p / rot_dim);
+    if (scaling == ORTHRUS_ROPE_LINEAR) {
+      f /= k;
+    } else if (ramp) {
+      double keep;
+      if (scaling == ORTHRUS_ROPE_BY_PARTS)
+        keep = (original * f / two_pi - (double)slow) / ((double)fast - (double)slow);
+      else
+        keep = 1.0 - (p - lo) / (hi - lo);
+      keep = std::min(std::max(keep, 0.0), 1.0);
+      f *= keep + (1.0 - keep) / k;
+    }
+    rope->turns[p] = f / two_pi;
+  }
+  return ORTHRUS_OK;
+}
+
+orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_part* parts, int32_t n_parts,
+                              int32_t batch, int32_t tokens, const int32_t* len, const int32_t* offsets,
+                              int32_t inverse, int32_t* status, orthrus_stream stream) {
+  if (!rope || !parts || n_parts < 1 || n_parts > ORTHRUS_ROTARY_MAX_PARTS || batch < 0 || tokens < 0)
+    return ORTHRUS_ERR_ARG;
+  if (rope->head_dim < 2 || rope->head_dim > 2 * kRotaryMaxPairs || rope->head_dim % 2 || rope->rot_dim < 2 ||
+      rope->rot_dim > rope->head_dim || rope->rot_dim % 2)
+    return ORTHRUS_ERR_ARG;
+  RotaryArgs a;
+  memcpy(a.turns, rope->turns, sizeof(a.turns));
+  // 16-byte accesses: units of 8 pairs, every address of a unit a multiple of 8 elements (of
+  // 4 for fp32, whose 8 values are two accesses; asked alike)
+  bool vec = rope->head_dim % 16 == 0 && rope->rot_dim % 16 == 0;
+  for (int i = 0; i < n_parts; ++i) {
+    const orthrus_rotary_part& p = parts[i];
+    if (!p.src || !p.dst || p.heads < 1 || p.group < 1 || p.heads % p.group || p.heads > 65536) return ORTHRUS_ERR_ARG;
+    for (const int t : {p.src_type, p.dst_type})
+      if (t != ORTHRUS_FP32 && t != ORTHRUS_BF16 && t != ORTHRUS_FP16) return ORTHRUS_ERR_ARG;
+    if (p.flags & ~(ORTHRUS_ROTARY_COPY | ORTHRUS_ROTARY_APPEND | ORTHRUS_ROTARY_BF16_VALUES)) return ORTHRUS_ERR_ARG;
+    if ((p.flags & ORTHRUS_ROTARY_APPEND) && p.rows < 1) return ORTHRUS_ERR_ARG;
+    if (!aligned(p.src, p.src_type == ORTHRUS_FP32 ? 4 : 2) || !aligned(p.dst, p.dst_type == ORTHRUS_FP32 ? 4 : 2))
+      return ORTHRUS_ERR_ARG;
+    vec = vec && aligned(p.src, 16) && aligned(p.dst, 16);
+    for (const int64_t s : {p.src_batch, p.src_token, p.src_head, p.dst_batch, p.dst_token, p.dst_kv, p.dst_head})
+      vec = vec && s % 8 == 0;
+    a.part[i] = p;
+  }
+  if (batch == 0 || tokens == 0) return ORTHRUS_OK;
+  a.n_parts = n_parts;
+  a.head_dim = rope->head_dim;
+  a.rot_dim = rope->rot_dim;
+  a.interleaved = rope->interleaved;
+  a.inverse = inverse;
+  a.gain = rope->gain;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.vec = vec;
+  a.total_items = 0;
+  const int per_head = rope->head_dim / (vec ? 16 : 2);
+  for (int i = 0; i < n_parts; ++i) {
+    a.items[i] = parts[i].heads * per_head;
+    a.total_items += a.items[i];
+  }
+  a.len = len;
+  a.offsets = offsets;
+  a.status = status;
+  const long long all = (long long)batch * tokens;
+  a.tok_per_cta = all >= 8 * num_sms() ? kRotaryTokens : 1;
+  const long long gx = (all + a.tok_per_cta - 1) / a.tok_per_cta;
+  if (gx > INT32_MAX) return ORTHRUS_ERR_ARG;
+  // few tokens: their heads are spread over up to eight CTAs
+  int gy = 1;
+  while (gy < 8 && gx * gy < num_sms() && gy * kRotaryThreads < a.total_items) gy *= 2;
+  return launch(rotary_kernel, dim3((unsigned)gx, gy), dim3(kRotaryThreads), 0, (cudaStream_t)stream, a) == cudaSuccess
+             ? ORTHRUS_OK
+             : ORTHRUS_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,20 +1,13 @@
 // Host side of liborthrus: plan construction (TMA descriptors encoded once),
 // launch geometry, the forward orchestration of the draft / verify / prefill
 // passes, and the C-ABI entry points declared in include/orthrus.h.
-#include <cuda.h>
-#include <cuda_runtime.h>
 #include <stdlib.h>
-#include <string.h>
-
-#include <algorithm>
-#include <cmath>
-#include <mutex>
-#include <utility>
-#include <vector>
 
 #include "attention.cuh"
 #include "forward.cuh"
 #include "gemm.cuh"
+#include "host.cuh"
+#include "operators.cuh"
 #include "orthrus.h"
 #include "sampling.cuh"
 #include "small.cuh"
@@ -23,141 +16,6 @@
 using namespace orthrus;
 
 namespace {
-
-// ---------------------------------------------------------------------------
-// driver entry point for tensor-map encoding (no link against libcuda)
-// ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeTiledFn)p;
-  }
-  return fn;
-}
-
-constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-
-// 2D map of 16-bit elements over a row-major [rows][cols] matrix; box = box_cols x box_rows,
-// 128-byte swizzle.
-bool map2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
-           CUtensorMapDataType dt = kBF16) {
-  EncodeTiledFn f = encode_fn();
-  if (!f || !base) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return f(m, dt, 2, const_cast<void*>(base), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 3D map of 16-bit elements over [z][rows][cols]; box = 64 cols x box_rows rows x box_z.
-bool map3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t z, uint32_t box_rows = 128,
-           uint32_t box_z = 1, CUtensorMapDataType dt = kBF16) {
-  EncodeTiledFn f = encode_fn();
-  if (!f || !base) return false;
-  cuuint64_t dims[3] = {cols, rows, z};
-  cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
-  cuuint32_t box[3] = {64, box_rows, box_z};
-  cuuint32_t es[3] = {1, 1, 1};
-  return f(m, dt, 3, const_cast<void*>(base), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// bf16 map of rank 3 or 4 with explicit strides (bytes, dims 1..rank-1) and box.
-bool map_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-            const uint32_t* box) {
-  EncodeTiledFn f = encode_fn();
-  if (!f || !base || rank < 3 || rank > 4) return false;
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4], es[4] = {1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-  }
-  for (int i = 0; i < rank - 1; ++i) st[i] = strides[i];
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, b, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 3-D view of a row-major [rows][cols] bf16 matrix as (64 columns, rows, cols/64 chunks) with
-// strides (row, 128 B): a box of (64, box_rows, 2) is two consecutive 64-wide k chunks.
-bool map_kpair(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
-  const uint64_t dims[3] = {64, rows, cols / 64};
-  const uint64_t strides[2] = {cols * 2, 128};
-  const uint32_t box[3] = {64, box_rows, 2};
-  return map_nd(m, base, 3, dims, strides, box);
-}
-
-// An activation in two planes [2][rows][cols] (hi, then lo), as (64 columns, rows, plane): a box
-// of (64, box_rows, 2) is one 64-wide k chunk of both planes.
-bool map_planes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
-  const uint64_t dims[3] = {cols, rows, 2};
-  const uint64_t strides[2] = {cols * 2, cols * rows * 2};
-  const uint32_t box[3] = {64, box_rows, 2};
-  return map_nd(m, base, 3, dims, strides, box);
-}
-
-// The same as (64 columns, rows, plane, cols/64 chunks): a box of (64, box_rows, 2, 2) is two
-// consecutive 64-wide k chunks of both planes, laid out [chunk][plane][row][64], so that per
-// chunk the hi rows and then the lo rows form one MMA operand of 2 box_rows rows.
-bool map_kpair_planes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
-  const uint64_t dims[4] = {64, rows, 2, cols / 64};
-  const uint64_t strides[3] = {cols * 2, cols * rows * 2, 128};
-  const uint32_t box[4] = {64, box_rows, 2, 2};
-  return map_nd(m, base, 4, dims, strides, box);
-}
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-int round_up(int x, int a) { return (x + a - 1) / a * a; }
-int next_pow2(int x) {
-  int p = 1;
-  while (p < x) p <<= 1;
-  return p;
-}
-
-int num_sms() {
-  static int n = 0;
-  if (!n) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-  }
-  return n;
-}
-
-constexpr size_t kSmemLimit = 232448;  // opt-in shared memory per CTA on sm_100
-
-// Programmatic dependent launch for every kernel: a kernel may begin its prologue and
-// weight loads while its predecessor drains; its griddepcontrol.wait orders everything else.
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
 
 // ---------------------------------------------------------------------------
 // plan
@@ -205,6 +63,9 @@ struct alignas(64) Plan {
   int ss_ld, mega_slots, fwd_ck;
   float* fwd_att_o;
   float2* fwd_att_ml;
+  // draft trees
+  int* tree_depth;
+  unsigned long long* tree_mask;
   size_t layers_off, maps_off, norms_off;
   // profiling hook (host memory, written during the calls)
   void* const* trace_ev;
@@ -275,7 +136,8 @@ int attn_chunk_keys(int B, int Hkv, int row_tiles, int cap) {
 // workspace layout
 struct WsLayout {
   size_t status, h, xn, qbuf, attn, act, rope, amax, draft_ids, ar_ids, samp, samp_tot, gemm_part, gemm_cnt, att_o, att_ml, att_cnt,
-      blk_k, blk_v, dev_maps, dev_norms, phase_cnt, ss, fwd_att_o, fwd_att_ml, total;
+      blk_k, blk_v, dev_maps, dev_norms, phase_cnt, ss, fwd_att_o, fwd_att_ml, tree_depth,
+      tree_mask, total;
   int chunk_keys, attn_slots, ss_ld, mega_slots;
 };
 
@@ -342,7 +204,8 @@ WsLayout ws_layout(const orthrus_config* c, int B, int max_block, int max_rows_r
   w.samp_tot = take((size_t)B * max_block * kSampMaxTiles * 4);
   w.gemm_part = take((size_t)2 * sms * 128 * 128 * 4);
   w.gemm_cnt = take((size_t)gemm_counter_count(c, max_rows) * 4);
-  w.att_o = take((size_t)w.attn_slots * 128 * d * 4);
+  // the chunk partials of the per-op attention, or the scratch of the tree attention
+  w.att_o = take(std::max((size_t)w.attn_slots * 128 * d * 4, tree_attn_scratch(B, Hkv, G, max_block, d)));
   w.att_ml = take((size_t)w.attn_slots * 128 * 8);
   w.att_cnt = take((size_t)std::max(B * Hkv * rt_dec, Hkv * rt_pre) * 4);
   const size_t blk = (size_t)L * B * Hkv * max_block * d * 2;
@@ -356,29 +219,10 @@ WsLayout ws_layout(const orthrus_config* c, int B, int max_block, int max_rows_r
   w.mega_slots = mega_slots(c, B, max_block);
   w.fwd_att_o = take((size_t)std::max(1, w.mega_slots) * kMaxChunks * 128 * d * 4);
   w.fwd_att_ml = take((size_t)std::max(1, w.mega_slots) * kMaxChunks * 128 * 8);
+  w.tree_depth = take((size_t)B * max_block * 4);
+  w.tree_mask = take((size_t)B * max_block * ((max_block + 63) / 64) * 8);
   w.total = off;
   return w;
-}
-
-template <typename F>
-bool set_smem_attr(F* kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
-// The dynamic shared-memory opt-in is a property of (kernel, device): it is set once per
-// pair, under a lock, so that host threads and calls on a second GPU each get it.
-template <typename F>
-bool ensure_smem_attr(F* kernel, size_t bytes) {
-  static std::mutex mu;
-  static std::vector<std::pair<int, const void*>> done;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const std::pair<int, const void*> key(dev, (const void*)kernel);
-  std::lock_guard<std::mutex> lock(mu);
-  if (std::find(done.begin(), done.end(), key) != done.end()) return true;
-  if (!set_smem_attr(kernel, bytes)) return false;
-  done.push_back(key);
-  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -569,17 +413,25 @@ orthrus_status launch_forward(const Plan* P, int view, int Q, const int* pending
   return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
 }
 
+// A draft tree's forward: the block's tokens, and its layout in the workspace.
+struct TreeBlock {
+  const int *tokens, *n_nodes;
+};
+
 // One forward over a block of Q rows for sequences [b0, b0+nb).
 //   kind: BLOCK_DRAFT / BLOCK_VERIFY / BLOCK_PREFILL
+//   tree: nullable; with BLOCK_VERIFY, the rows are a tree's nodes (all sequences): positions by
+//   depth, K/V to the block scratch, attention by the visibility words
 //   head: run final norm + LM head + argmax; last_row_only: only row Q-1 of each sequence
 //   argmax_out: [rows of the head] int32; logits: nullable fp32 [rows][vocab]
 orthrus_status forward(const Plan* P, int kind, int b0, int nb, int Q, const int* pending, const int* draft,
                        const int* tokens, int tok_stride, int tok_off, bool head, bool last_row_only, int* argmax_out,
-                       float* logits, cudaStream_t st) {
+                       float* logits, cudaStream_t st, const TreeBlock* tree = nullptr) {
   const orthrus_config& c = P->cfg;
   const int D = c.d_model, H = c.n_heads, Hkv = c.n_kv_heads, d = c.head_dim, F = c.d_ff, V = c.vocab;
   const int G = H / Hkv, M = nb * Q;
   const bool draft_view = kind == BLOCK_DRAFT;
+  const bool to_scratch = draft_view || tree != nullptr;  // where the block's K/V go
 
   EmbedArgs ea;
   ea.kind = kind;
@@ -603,7 +455,27 @@ orthrus_status forward(const Plan* P, int kind, int b0, int nb, int Q, const int
   ea.rope = P->rope;
   ea.status = P->status;
   mark(P, ORTHRUS_KIND_EMBED, st);
-  if (launch(embed_kernel, dim3(M), dim3(256), 0, st, ea) != cudaSuccess) return ORTHRUS_ERR_CUDA;
+  if (tree) {
+    TreeEmbedArgs te;
+    te.nodes = Q;
+    te.D = D;
+    te.d = d;
+    te.V = V;
+    te.theta = (double)c.rope_theta;
+    te.pending = pending;
+    te.tokens = tree->tokens;
+    te.n_nodes = tree->n_nodes;
+    te.depth = P->tree_depth;
+    te.len = P->len;
+    te.embed = P->embed;
+    te.h = P->h;
+    te.rope = P->rope;
+    te.status = P->status;
+    const orthrus_status es = launch_tree_embed(te, M, st);
+    if (es != ORTHRUS_OK) return es;
+  } else if (launch(embed_kernel, dim3(M), dim3(256), 0, st, ea) != cudaSuccess) {
+    return ORTHRUS_ERR_CUDA;
+  }
 
   AttnArgs aa;
   memset(&aa, 0, sizeof(aa));
@@ -627,7 +499,7 @@ orthrus_status forward(const Plan* P, int kind, int b0, int nb, int Q, const int
   aa.part_ml = P->att_ml;
   aa.counter = P->att_cnt;
   aa.status = P->status;
-  if ((long long)nb * Hkv * aa.row_tiles * aa.max_chunks > P->attn_slots) return ORTHRUS_ERR_WORKSPACE;
+  if (!tree && (long long)nb * Hkv * aa.row_tiles * aa.max_chunks > P->attn_slots) return ORTHRUS_ERR_WORKSPACE;
 
   for (int l = 0; l < P->L; ++l) {
     const LayerPtrs& lp = P->layer(l);
@@ -643,14 +515,14 @@ orthrus_status forward(const Plan* P, int kind, int b0, int nb, int Q, const int
     g.qkv.Q = Q;
     g.qkv.b0 = b0;
     g.qkv.qk_norm = c.qk_norm;
-    g.qkv.mode = draft_view ? VIEW_DRAFT : VIEW_VERIFY;
+    g.qkv.mode = to_scratch ? VIEW_DRAFT : VIEW_VERIFY;
     g.qkv.eps = c.rms_eps;
     g.qkv.gq = draft_view ? lp.wd_q_norm : lp.q_norm;
     g.qkv.gk = draft_view ? lp.wd_k_norm : lp.k_norm;
     g.qkv.rope = P->rope;
     g.qkv.len = P->len;
     g.qkv.qbuf = P->qbuf;
-    if (draft_view) {
+    if (to_scratch) {
       const size_t lo = (size_t)l * P->B * Hkv * P->max_block * d;
       g.qkv.kdst = P->blk_k + lo;
       g.qkv.vdst = P->blk_v + lo;
@@ -670,9 +542,38 @@ orthrus_status forward(const Plan* P, int kind, int b0, int nb, int Q, const int
     aa.z_cache = l * P->B * Hkv;
     aa.z_blk = l * P->B * Hkv;
     mark(P, ORTHRUS_KIND_ATTENTION, st);
-    if ((launch_attention(d, P->gmap(G_Q), P->gmap(G_KC), P->gmap(G_VC), P->gmap(G_KB), P->gmap(G_VB), aa, st)) !=
-        cudaSuccess)
+    if (tree) {
+      const size_t zc = (size_t)l * P->B * Hkv * P->cap * d, zb = (size_t)l * P->B * Hkv * P->max_block * d;
+      TreeAttnArgs ta;
+      memset(&ta, 0, sizeof(ta));
+      ta.q = P->qbuf;
+      ta.k_cache = P->kc + zc;
+      ta.v_cache = P->vc + zc;
+      ta.k_blk = P->blk_k + zb;
+      ta.v_blk = P->blk_v + zb;
+      ta.len = P->len;
+      ta.n_nodes = nullptr;  // padding rows are computed too (they see the cache): the projections read every row
+      ta.mask = P->tree_mask;
+      ta.B = nb;
+      ta.Hkv = Hkv;
+      ta.G = G;
+      ta.N = Q;
+      ta.d = d;
+      ta.cap = P->cap;
+      ta.blk_stride = P->max_block;
+      ta.words = (Q + 63) / 64;
+      ta.bf16 = 0;
+      ta.out_type = ORTHRUS_BF16_PLANES;
+      ta.scale_log2 = aa.scale_log2;
+      ta.out = P->attn;
+      ta.out_lo = P->attn_lo;
+      ta.status = P->status;
+      const orthrus_status ts = launch_tree_attention(ta, P->att_o, st);
+      if (ts != ORTHRUS_OK) return ts;
+    } else if ((launch_attention(d, P->gmap(G_Q), P->gmap(G_KC), P->gmap(G_VC), P->gmap(G_KB), P->gmap(G_VB), aa,
+                                 st)) != cudaSuccess) {
       return ORTHRUS_ERR_CUDA;
+    }
 
     g = base_gemm_args(P);
     g.out_f32 = P->h;
@@ -844,6 +745,8 @@ orthrus_status orthrus_plan_init(void* plan, size_t plan_bytes, const orthrus_co
   }
   P->fwd_att_o = (float*)(base + wl.fwd_att_o);
   P->fwd_att_ml = (float2*)(base + wl.fwd_att_ml);
+  P->tree_depth = (int*)(base + wl.tree_depth);
+  P->tree_mask = (unsigned long long*)(base + wl.tree_mask);
   P->norms_off = norms_off;
   P->layers_off = layers_off;
   P->maps_off = maps_off;
@@ -1408,3 +1311,43 @@ extern "C" orthrus_status orthrus_linear_noalloc(const void* X, const void* W, f
   return launch_gemm_capped<EPI_STORE>(tw, tx, a, N, Kd, M, kNoAllocCtas, st) == cudaSuccess ? ORTHRUS_OK
                                                                                             : ORTHRUS_ERR_CUDA;
 }
+
+// ---------------------------------------------------------------------------
+// draft trees with a plan
+// ---------------------------------------------------------------------------
+extern "C" {
+
+orthrus_status orthrus_verify_tree(const void* plan, const int32_t* pending, const int32_t* tokens,
+                                   const int32_t* parents, const int32_t* n_nodes, int32_t nodes, int32_t* argmax,
+                                   float* logits, orthrus_stream stream) {
+  const Plan* P = plan_cast(plan);
+  if (!P || !pending || !tokens || !parents || !argmax || nodes < 1 || nodes > P->max_block ||
+      !tree_sizes_ok(P->B, nodes))
+    return ORTHRUS_ERR_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  mark(P, ORTHRUS_KIND_OTHER, st);
+  orthrus_status s = launch_tree_layout(parents, n_nodes, P->B, nodes, P->tree_depth, P->tree_mask, P->status, st);
+  if (s != ORTHRUS_OK) return s;
+  const TreeBlock tree = {tokens, n_nodes};
+  s = forward(P, BLOCK_VERIFY, 0, P->B, nodes, pending, nullptr, nullptr, 0, 0, true, false, argmax, logits, st, &tree);
+  mark(P, ORTHRUS_KIND_END, st);
+  return s;
+}
+
+orthrus_status orthrus_accept_commit_tree(const void* plan, int32_t* pending, const int32_t* tokens,
+                                          const int32_t* parents, const int32_t* n_nodes, const int32_t* argmax,
+                                          int32_t nodes, int32_t* accept_len, int32_t* path, int32_t* committed,
+                                          orthrus_stream stream) {
+  const Plan* P = plan_cast(plan);
+  if (!P || nodes < 1 || nodes > P->max_block) return ORTHRUS_ERR_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  mark(P, ORTHRUS_KIND_ACCEPT, st);
+  const orthrus_status s =
+      orthrus_tree_commit(parents, tokens, argmax, n_nodes, P->blk_k, P->blk_v, P->max_block, P->kc, P->vc, P->L, P->B,
+                          P->cfg.n_kv_heads, P->cap, P->cfg.head_dim, nodes, P->len, P->len, pending, accept_len, path,
+                          committed, P->status, stream);
+  mark(P, ORTHRUS_KIND_END, st);
+  return s;
+}
+
+}  // extern "C"

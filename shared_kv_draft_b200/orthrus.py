@@ -11,7 +11,9 @@ host arrays, the KV cache, the workspace) and the host plan buffer.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
+from builtins import len as _length  # some calls below have an argument `len`, the cache lengths
 
 import numpy as np
 import torch
@@ -57,6 +59,23 @@ class AcceptStats(C.Structure):
     _fields_ = [("accepted", C.c_float), ("rejected", C.c_float)]
 
 
+FP32, BF16, FP16, BF16_PLANES = range(4)
+ROTARY_MAX_PARTS, ROTARY_COPY, ROTARY_APPEND, ROTARY_BF16_VALUES = 3, 1, 2, 4
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2, "by_index": 3}
+TREE_MAX_NODES, TREE_MAX_BATCH = 256, 1024
+
+
+class Rope(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("gain", C.c_float),
+                ("turns", C.c_double * 128)]
+
+
+class RotaryPart(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p)] + [
+        (n, C.c_int32) for n in ("src_type", "dst_type", "heads", "group", "flags", "rows")] + [
+        (n, C.c_int64) for n in ("src_batch", "src_token", "src_head", "dst_batch", "dst_token", "dst_kv", "dst_head")]
+
+
 # (name, restype, argtypes) for every symbol of include/orthrus.h
 _I32, _SZ, _VP, _F = C.c_int32, C.c_size_t, C.c_void_p, C.c_float
 _PCFG = C.POINTER(Config)
@@ -92,6 +111,16 @@ SIGNATURES = [
     ("orthrus_accept_stats_update", _I32, [_PST, _VP, _I32, _I32, _F]),
     ("orthrus_accept_rate", _F, [_PST]),
     ("orthrus_choose_block_size", _I32, [_PST, _I32, _VP, _VP, _I32]),
+    ("orthrus_tree_layout", _I32, [_VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP]),
+    ("orthrus_tree_attention_workspace_bytes", _SZ, [_I32, _I32, _I32, _I32, _I32]),
+    ("orthrus_tree_attention", _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                      _I32, _I32, _F, _VP, _VP, _SZ, _VP, _VP]),
+    ("orthrus_tree_commit", _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32,
+                                   _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    ("orthrus_verify_tree", _I32, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
+    ("orthrus_accept_commit_tree", _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP]),
+    ("orthrus_rope_init", _I32, [_VP, _I32, _I32, _I32, _F, _I32, _F, _I32, _F, _F, _F]),
+    ("orthrus_rotary", _I32, [_VP, _VP, _I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP]),
 ]
 
 _lib = None
@@ -226,6 +255,183 @@ def linear_workspace_bytes(M, N, Kd) -> int:
     return load().orthrus_linear_workspace_bytes(M, N, Kd)
 
 
+# ---- draft trees and rotary positions ------------------------------------------------------------
+
+_TYPES = {torch.float32: FP32, torch.bfloat16: BF16, torch.float16: FP16}
+
+
+class _Call:
+    """The stream a call runs on: `stream`, or the current stream of the device that holds its
+    tensors, which is made the current device for the call where it is another one."""
+
+    def __init__(self, device, stream):
+        self.index = device.index
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.back = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.index != now:
+            self.back = now
+            torch.cuda.set_device(self.index)
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _arg(ok, call, what):
+    if not ok:
+        raise ValueError(f"{call}: {what}")
+
+
+def _dense(call, device, dtype, **tensors):
+    """Every given tensor lies densely on `device` with `dtype` (None passes where it is optional)."""
+    for name, t in tensors.items():
+        _arg(t is None or (t.dtype is dtype and t.device == device and t.is_contiguous()), call,
+             f"{name} must be a contiguous {dtype} tensor on {device}")
+
+
+def tree_layout(parents, depth, mask, n_nodes=None, status=None, stream=None):
+    """Depths and visibility words of draft trees. parents: int32 [B][N]; depth: int32 [B][N]; mask:
+    int64 [B][N][ceil(N / 64)] (the words' bits)."""
+    dev, name = parents.device, "tree_layout"
+    _arg(parents.dim() == 2 and parents.is_cuda, name, "parents must be [batch][nodes] on a GPU")
+    B, N = parents.shape
+    _dense(name, dev, torch.int32, parents=parents, depth=depth, n_nodes=n_nodes, status=status)
+    _dense(name, dev, torch.int64, mask=mask)
+    _arg(depth.shape == parents.shape and mask.shape == (B, N, (N + 63) // 64), name, "depth or mask has another shape")
+    _arg(n_nodes is None or n_nodes.shape == (B,), name, "n_nodes must be [batch]")
+    with _Call(dev, stream) as st:
+        code = load().orthrus_tree_layout(_ptr(parents), _ptr(n_nodes), B, N, _ptr(depth), _ptr(mask), _ptr(status), st)
+    _check("orthrus_tree_layout", code)
+
+
+def tree_attention_workspace_bytes(batch, n_kv_heads, group, nodes, head_dim) -> int:
+    return load().orthrus_tree_attention_workspace_bytes(batch, n_kv_heads, group, nodes, head_dim)
+
+
+def tree_attention(q, k_cache, v_cache, k_blk, v_blk, len, mask, out, workspace, n_nodes=None, scale=0.0, status=None,
+                   stream=None):
+    """Attention of draft trees over one layer's cache. q: [B][Hkv][N*G][d]; k_cache, v_cache:
+    [B][Hkv][capacity][d]; k_blk, v_blk: [B][Hkv][>= N][d], all fp16 or all bf16; len: int32 [B]; mask: int64
+    [B][N][words]; out: fp16 or bf16 [B*N][H*d], or bf16 [2][B*N][H*d] (hi and lo plane); workspace:
+    uint8, tree_attention_workspace_bytes() or more."""
+    dev, t, name = q.device, q.dtype, "tree_attention"
+    _arg(q.dim() == 4 and q.is_cuda and t in (torch.float16, torch.bfloat16), name,
+         "q must be fp16 or bf16 [batch][kv heads][nodes*group][d] on a GPU")
+    B, H, R, d = q.shape
+    _dense(name, dev, t, q=q, k_cache=k_cache, v_cache=v_cache, k_blk=k_blk, v_blk=v_blk)
+    _arg(mask.dim() == 3 and mask.shape[0] == B and mask.shape[1] > 0, name, "mask must be [batch][nodes][words]")
+    N = mask.shape[1]
+    _dense(name, dev, torch.int64, mask=mask)
+    _arg(mask.shape[2] == (N + 63) // 64 and R % N == 0, name, "mask does not fit q")
+    _dense(name, dev, torch.int32, len=len, n_nodes=n_nodes, status=status)
+    _arg(len.shape == (B,) and (n_nodes is None or n_nodes.shape == (B,)), name, "len and n_nodes must be [batch]")
+    for c, least in ((k_cache, 1), (k_blk, N)):
+        _arg(c.dim() == 4 and c.shape[:2] == (B, H) and c.shape[2] >= least and c.shape[3] == d, name,
+             "a cache or block has another shape")
+    _arg(v_cache.shape == k_cache.shape and v_blk.shape == k_blk.shape, name, "K and V must have one shape")
+    planes = out.dim() == 3
+    _arg(out.shape == ((2, B * N, H * (R // N) * d) if planes else (B * N, H * (R // N) * d))
+         and (out.dtype is torch.bfloat16 or (out.dtype is torch.float16 and not planes)), name,
+         "out must be [batch*nodes][heads*d] in fp16 or bf16, or two such planes in bf16")
+    _dense(name, dev, out.dtype, out=out)
+    _dense(name, dev, workspace.dtype, workspace=workspace)
+    with _Call(dev, stream) as st:
+        code = load().orthrus_tree_attention(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_blk.data_ptr(), v_blk.data_ptr(), len.data_ptr(),
+            _ptr(n_nodes), mask.data_ptr(), B, H, R // N, N, d, k_cache.shape[2], k_blk.shape[2], _TYPES[t],
+            BF16_PLANES if planes else _TYPES[out.dtype], scale, out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(status), st)
+    _check("orthrus_tree_attention", code)
+
+
+def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, new_len, pending, accept_len, path,
+                committed, n_nodes=None, status=None, stream=None):
+    """Greedy consensus on draft trees and the accepted paths' K/V rows into the cache. k_blk, v_blk:
+    [L][B][Hkv][>= N][d] and k_cache, v_cache: [L][B][Hkv][capacity][d] of one 16-bit type; the others int32, [B] or
+    [B][N]. new_len may be len."""
+    dev, name = parents.device, "tree_commit"
+    _arg(parents.dim() == 2 and parents.is_cuda, name, "parents must be [batch][nodes] on a GPU")
+    B, N = parents.shape
+    _dense(name, dev, torch.int32, parents=parents, tokens=tokens, argmax=argmax, path=path, committed=committed, len=len,
+           new_len=new_len, pending=pending, accept_len=accept_len, n_nodes=n_nodes, status=status)
+    for t in (tokens, argmax, path, committed):
+        _arg(t.shape == (B, N), name, "tokens, argmax, path and committed must be [batch][nodes]")
+    for t in (len, new_len, pending, accept_len, n_nodes):
+        _arg(t is None or t.shape == (B,), name, "len, new_len, pending, accept_len and n_nodes must be [batch]")
+    _arg(k_cache.dim() == 5 and k_blk.dim() == 5 and k_cache.element_size() == 2, name,
+         "caches and blocks must be five-dimensional with 16-bit elements")
+    L, _, H, cap, d = k_cache.shape
+    _dense(name, dev, k_cache.dtype, k_blk=k_blk, v_blk=v_blk, k_cache=k_cache, v_cache=v_cache)
+    _arg(k_cache.shape == v_cache.shape and k_blk.shape == v_blk.shape and k_cache.shape[1] == B
+         and k_blk.shape[:3] == (L, B, H) and k_blk.shape[3] >= N and k_blk.shape[4] == d, name,
+         "a cache or block has another shape")
+    with _Call(dev, stream) as st:
+        code = load().orthrus_tree_commit(
+            parents.data_ptr(), tokens.data_ptr(), argmax.data_ptr(), _ptr(n_nodes), k_blk.data_ptr(), v_blk.data_ptr(),
+            k_blk.shape[3], k_cache.data_ptr(), v_cache.data_ptr(), L, B, H, cap, d, N, len.data_ptr(),
+            new_len.data_ptr(), pending.data_ptr(), accept_len.data_ptr(), path.data_ptr(), committed.data_ptr(),
+            _ptr(status), st)
+    _check("orthrus_tree_commit", code)
+
+
+@functools.lru_cache(maxsize=64)
+def rope(head_dim, rot_dim=None, theta=1.0e6, interleaved=False, scaling="none", factor=1.0, original=1, slow=1.0,
+         fast=32.0, gain=0.0) -> Rope:
+    """Frequencies of a rotary embedding (host only): the table for rotary(). The same arguments give the same
+    table object; it is not to be changed (fill a Rope for frequencies of one's own)."""
+    r = Rope()
+    _arg(scaling in ROPE_SCALINGS, "rope", f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    _check("orthrus_rope_init",
+           load().orthrus_rope_init(C.byref(r), head_dim, head_dim if rot_dim is None else rot_dim, int(bool(interleaved)),
+                                    theta, ROPE_SCALINGS[scaling], factor, original, slow, fast, gain))
+    return r
+
+
+def rotary(rope, parts, len=None, offsets=None, inverse=False, status=None, stream=None):
+    """Turn heads at positions len[b] + offsets[b][t] (0 and t where they are None).
+
+    parts: up to three (src, dst) or (src, dst, flags). src: [B][T][heads][d]; dst: [B][rows][heads][d], or
+    [B][rows][kv heads][group][d]; views with any strides, the last dimension dense; fp32, bf16 or fp16.
+    rows = T, or with ROTARY_APPEND the rows of the cache that rows len[b] + t are written to. ROTARY_COPY:
+    no rotation; ROTARY_BF16_VALUES: rounded to bf16 first. inverse: back by the same angles (the gradient)."""
+    name = "rotary"
+    n = _length(parts)
+    _arg(1 <= n <= ROTARY_MAX_PARTS, name, f"1 to {ROTARY_MAX_PARTS} parts")
+    dev = parts[0][0].device
+    B, T = parts[0][0].shape[:2]
+    arr = (RotaryPart * n)()
+    for a, part in zip(arr, parts):
+        src, dst = part[0], part[1]
+        flags = part[2] if _length(part) > 2 else 0
+        _arg(src.is_cuda and src.device == dev and dst.device == dev, name, "all tensors must be on one GPU")
+        _arg(src.dtype in _TYPES and dst.dtype in _TYPES, name, "tensors must be fp32, bf16 or fp16")
+        ss, ds, shape = src.stride(), dst.stride(), dst.shape
+        _arg(src.dim() == 4 and src.shape[:2] == (B, T) and src.shape[3] == rope.head_dim and ss[3] == 1, name,
+             "src must be [batch][tokens][heads][d] with a dense last dimension")
+        heads = src.shape[2]
+        grouped = dst.dim() == 5
+        _arg((grouped or dst.dim() == 4) and shape[0] == B and shape[-1] == rope.head_dim and ds[-1] == 1
+             and (shape[2] * shape[3] if grouped else shape[2]) == heads
+             and (flags & ROTARY_APPEND or shape[1] == T), name,
+             "dst must be [batch][rows][heads][d] or [batch][rows][kv heads][group][d] with a dense last dimension")
+        a.src, a.dst, a.src_type, a.dst_type = src.data_ptr(), dst.data_ptr(), _TYPES[src.dtype], _TYPES[dst.dtype]
+        a.heads, a.group, a.flags, a.rows = heads, shape[3] if grouped else 1, flags, shape[1]
+        a.src_batch, a.src_token, a.src_head = ss[:3]
+        a.dst_batch, a.dst_token, a.dst_kv = ds[:3]
+        a.dst_head = ds[3] if grouped else 0
+    _dense(name, dev, torch.int32, len=len, offsets=offsets, status=status)
+    _arg((len is None or len.shape == (B,)) and (offsets is None or offsets.shape == (B, T)), name,
+         "len must be [batch] and offsets [batch][tokens]")
+    with _Call(dev, stream) as st:
+        code = load().orthrus_rotary(C.byref(rope), arr, n, B, T, _ptr(len), _ptr(offsets), int(bool(inverse)),
+                                     _ptr(status), st)
+    _check("orthrus_rotary", code)
+
+
 # ---- a plan with its device buffers --------------------------------------------------------------
 
 _LAYER_FIELDS = [("attn_norm", "attn_norm"), ("mlp_norm", "mlp_norm"), ("w_qkv", "w_qkv"), ("w_o", "w_o"),
@@ -333,6 +539,19 @@ class DeviceModel:
                                                   _ptr(u_accept), _ptr(u_final), _ptr(draft_logits),
                                                   _ptr(verify_logits), _ptr(accept_len), _ptr(committed),
                                                   _stream(stream)))
+
+    def verify_tree(self, pending, tokens, parents, argmax, n_nodes=None, logits=None, stream=None):
+        """tokens, parents, argmax: device int32 [batch][nodes]; n_nodes: device int32 [batch] or None."""
+        _check("orthrus_verify_tree",
+               load().orthrus_verify_tree(self.plan, _ptr(pending), _ptr(tokens), _ptr(parents), _ptr(n_nodes),
+                                          tokens.shape[1], _ptr(argmax), _ptr(logits), _stream(stream)))
+
+    def accept_commit_tree(self, pending, tokens, parents, argmax, accept_len, path, committed, n_nodes=None,
+                           stream=None):
+        _check("orthrus_accept_commit_tree",
+               load().orthrus_accept_commit_tree(self.plan, _ptr(pending), _ptr(tokens), _ptr(parents), _ptr(n_nodes),
+                                                 _ptr(argmax), tokens.shape[1], _ptr(accept_len), _ptr(path),
+                                                 _ptr(committed), _stream(stream)))
 
     def clear_status(self, stream=None):
         _check("orthrus_clear_status", load().orthrus_clear_status(self.plan, _stream(stream)))
