@@ -13,18 +13,47 @@ bool orthrus::tree_sizes_ok(int batch, int nodes) {
   return batch >= 1 && batch <= ORTHRUS_TREE_MAX_BATCH && nodes >= 1 && nodes <= ORTHRUS_TREE_MAX_NODES;
 }
 
+// Two parts for each CTA: of the unit in which its range starts, and of the one in which it ends.
 size_t orthrus::tree_attn_scratch(int B, int Hkv, int G, int nodes, int d) {
-  (void)B, (void)Hkv, (void)G, (void)nodes, (void)d;
-  return 256;
+  (void)B, (void)Hkv, (void)G, (void)nodes;
+  return (size_t)2 * num_sms() * kTreeRows * ((size_t)d * 4 + 8);
 }
 
-orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& a, void* workspace, cudaStream_t st) {
-  (void)workspace;
-  const long long rows = (long long)a.B * a.Hkv * a.N * a.G;
-  const dim3 grid((unsigned)((rows + 3) / 4));
-  const cudaError_t e = a.d == 128 ? launch(tree_attention_kernel<128>, grid, dim3(128), 0, st, a)
-                                   : launch(tree_attention_kernel<64>, grid, dim3(128), 0, st, a);
-  return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
+namespace {
+
+template <int D, bool BF16>
+orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  if (!ensure_smem_attr(tree_attention_kernel<D, BF16>, TreeSmem<D>::kBytes)) return ORTHRUS_ERR_CUDA;
+  const int sms = num_sms();
+  if (launch(tree_attention_kernel<D, BF16>, dim3(sms), dim3(kTreeThreads), TreeSmem<D>::kBytes, st, m[0], m[1], m[2],
+             m[3], m[4], a) != cudaSuccess)
+    return ORTHRUS_ERR_CUDA;
+  const int rows = std::min(kTreeRows, a.N * a.G);
+  return launch(tree_combine_kernel, dim3(sms - 1, (rows + 31) / 32, D / 32), dim3(kJoinThreads), 0, st, a, sms) ==
+                 cudaSuccess
+             ? ORTHRUS_OK
+             : ORTHRUS_ERR_CUDA;
+}
+
+}  // namespace
+
+orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* workspace, cudaStream_t st) {
+  if (!encode_fn()) return ORTHRUS_ERR_CUDA;
+  TreeAttnArgs a = args;
+  a.part_o = (float4*)workspace;
+  a.part_ml = (float2*)(a.part_o + (size_t)2 * num_sms() * kTreeRows * (a.d / 4));
+  const CUtensorMapDataType dt = a.bf16 ? kBF16 : kF16;
+  const uint64_t z = (uint64_t)a.B * a.Hkv;
+  CUtensorMap m[5];
+  const bool ok = map2d(&m[0], a.q, a.d, z * a.N * a.G, 64, 128, dt) &&
+                  map3d(&m[1], a.k_cache, a.d, a.cap, z, kTreeKeys, 1, dt) &&
+                  map3d(&m[2], a.v_cache, a.d, a.cap, z, kTreeKeys, 1, dt) &&
+                  map3d(&m[3], a.k_blk, a.d, a.blk_stride, z, kTreeKeys, 1, dt) &&
+                  map3d(&m[4], a.v_blk, a.d, a.blk_stride, z, kTreeKeys, 1, dt);
+  if (!ok) return ORTHRUS_ERR_ARG;
+  if (a.d == 128)
+    return a.bf16 ? launch_tree_attention_as<128, true>(a, m, st) : launch_tree_attention_as<128, false>(a, m, st);
+  return a.bf16 ? launch_tree_attention_as<64, true>(a, m, st) : launch_tree_attention_as<64, false>(a, m, st);
 }
 
 orthrus_status orthrus::launch_tree_layout(const int* parents, const int* n_nodes, int batch, int nodes, int* depth,

@@ -16,6 +16,9 @@ struct TreeAttnArgs {
   void* out;
   size_t out_lo;  // ORTHRUS_BF16_PLANES: elements from the hi to the lo plane
   int* status;
+  // scratch, laid out by launch_tree_attention
+  float4* part_o;   // [2 per CTA][d / 4][256 rows]
+  float2* part_ml;  // [2 per CTA][256 rows]: (reference, sum of weights)
 };
 
 // Embedding of a tree block: row m = b * nodes + i at position len[b] + depth[i]; node 0 is

@@ -1,71 +1,744 @@
-// Attention of a draft tree over the KV cache and the tree's own K/V.
+// Attention of a draft tree over the KV cache and the tree's own K/V, on tcgen05.
 //
 // Row (i, g) of KV head h (query head h G + g at tree node i) sees the cache rows
 // [0, len[b]) and the tree rows j whose bit is set in the node's visibility words:
-//     out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - m)
-// with the running maximum m and sum in fp32; a row that sees nothing gives zeros.
+//     out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(s_j - m),   s_j = log2(e) scale q.k_j
+// in one pass over the keys with a running reference m per row; a row that sees nothing
+// gives zeros.
+//
+// Bound: the cache is read once, so HBM for trees of up to 256 rows (nodes x group) per KV
+// head; at 256 rows the two matrix products need as long as the reads.
+//
+// Split. A unit is (sequence, KV head, group of up to 256 rows); its keys come in tiles of
+// 128, cache tiles first, then the tree's. All tiles of all units form one line, cut into
+// equal contiguous ranges, one per CTA and at most one CTA per SM: a ragged batch loads
+// every SM alike, with lengths known only on the device. A unit that lies in one range is
+// finished there; of a unit that is cut, each CTA stores its part (unnormalised sums, the
+// reference and the weights' sum per row, fp32), and tree_combine_kernel joins the parts in
+// key order. The cut depends on the lengths alone, so results repeat bit for bit.
+//
+// One CTA: warp 8 loads (TMA, ring of 128-key K and V tiles), warp 9 issues the MMAs, warps
+// 0-3 and 4-7 are two softmax streams, one thread per row. TMEM holds S0, S1 (128 columns
+// each) and O0, O1; P (16 bit) overwrites its S and is read by the second product from there.
+//   More than 128 rows: stream s owns rows [128 s, 128 s + 128) of the group and sees every
+//   tile, so a K/V tile is loaded once for both.
+//   At most 128 rows: both streams own the same rows and take the tiles in turn; their sums
+//   are joined when the segment ends.
+// Either way one stream's softmax runs under the other's products.
+//
+// The accumulators stay in TMEM. The reference m of a row moves only when a tile's maximum
+// exceeds it by more than 8 (a factor of 256), and only then is O rescaled. Weights carry a
+// factor 2^7 that cancels in the quotient: between 2^15 (below fp16's 65504) and fp16's
+// smallest step 2^-24 they keep 39 binades below the largest possible one. Scores, sums and
+// the quotient are fp32; P is rounded to the operands' type for its product with V, because
+// the tensor cores take 16-bit operands of one type: half a step, 2^-11 (fp16) or 2^-8 (bf16)
+// of each weight.
+//
+// Rows of K and V that no row may see (past len, past the tree) can hold anything: their
+// scores are replaced and their V rows are zeroed in shared memory before the product. A V
+// value that is not finite in a live tree row is zeroed as well and added afterwards to the
+// rows that see that node, so that 0 x NaN reaches nobody else.
 #pragma once
 #include "operators.cuh"
 #include "ptx.cuh"
 
 namespace orthrus {
 
-__device__ __forceinline__ void tree_store(const TreeAttnArgs& a, size_t at, float x) {
-  if (a.out_type == ORTHRUS_FP16) {
-    ((__half*)a.out)[at] = __float2half_rn(x);
+constexpr int kTreeThreads = 384;   // two softmax warpgroups; one with the load and the MMA warp
+// Registers a thread: 384 threads are launched with 168 each (64512); the softmax warps hold a row of
+// scores in registers and take 208, the others give theirs up: 256 x 208 + 128 x 88 = 64512.
+constexpr int kTreeRegs = 208, kTreeRegsOther = 88;
+constexpr int kTreeKeys = 128;      // keys of a tile
+constexpr int kTreeRows = 256;      // rows of a unit
+constexpr float kTreeSlack = 8.f;   // how far scores may exceed the reference (log2)
+constexpr float kTreeShift = 7.f;   // factor on the weights (log2)
+constexpr int kTreeLoadWarp = 8, kTreeMmaWarp = 9;
+
+template <int D>
+struct TreeSmem {
+  static constexpr int kTile = kTreeKeys * D * 2;  // bytes of a K, V or Q tile
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kMisc = kRing + kStages * kTile;
+  static constexpr int kBytes = 1024 + kMisc + 2048;  // 1024: alignment of the dynamic part
+};
+
+struct TreeStart {  // where a CTA's range of tiles starts
+  long long scan[kTreeThreads / 32], off;
+  int b;
+};
+
+struct TreeMisc {
+  uint64_t full[10], empty[10], q_full, q_empty, s_full[2], p_full[2], o_done[2], done;
+  uint32_t tmem;
+  int ok[2];            // per stream: the last wait of its leader succeeded
+  int bad_any;
+  unsigned int bad[8];  // tree rows with values that are not finite (this segment)
+  TreeStart start;
+  float2 ml[128];       // one stream's (reference, sum) for the other
+};
+static_assert(sizeof(TreeMisc) <= 2048, "misc area");
+
+// ---- the line of tiles --------------------------------------------------------------------
+
+struct TreeSeq {
+  int n, live, tiles, groups;  // clamped length, nodes, tiles of a unit, row groups
+  __device__ TreeSeq() {}
+  __device__ TreeSeq(const TreeAttnArgs& a, int b) {
+    n = min(max(a.len[b], 0), a.cap);
+    live = a.n_nodes ? min(max(a.n_nodes[b], 0), a.N) : a.N;
+    groups = (live * a.G + kTreeRows - 1) / kTreeRows;
+    tiles = (n + kTreeKeys - 1) / kTreeKeys + (live + kTreeKeys - 1) / kTreeKeys;
+  }
+  __device__ long long work(int Hkv) const { return (long long)groups * Hkv * tiles; }
+};
+
+__device__ __forceinline__ long long tree_cut(long long total, int ctas, int c) { return total * c / ctas; }
+
+// Finds the start of range c of the line of tiles: sequence st.b and tile st.off among that
+// sequence's (st.b = -1 if the range is empty). Returns all tiles, the ranges and the bounds of
+// this one. Called by all THREADS threads of the CTA; the sums before each sequence are an
+// exclusive scan over the CTA, every thread holding a contiguous share of the sequences.
+template <int THREADS>
+__device__ __forceinline__ void tree_start(const TreeAttnArgs& a, TreeStart& st, int c, int sms, bool check,
+                                           long long& total, int& ctas, long long& w0, long long& w1) {
+  const int per = (a.B + THREADS - 1) / THREADS;
+  const int lo = min(a.B, (int)threadIdx.x * per), hi = min(a.B, lo + per);
+  long long own = 0;
+  for (int b = lo; b < hi; ++b) {
+    own += TreeSeq(a, b).work(a.Hkv);
+    const int n = a.len[b];
+    if (check && (n < 0 || n > a.cap)) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
+  }
+  long long inc = own;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) st.scan[warp] = inc;
+  if (threadIdx.x == 0) st.b = -1;
+  __syncthreads();
+  long long at = inc - own;
+  total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) at += st.scan[w];
+    total += st.scan[w];
+  }
+  ctas = (int)max(1ll, min((long long)sms, total));
+  w0 = c < ctas ? tree_cut(total, ctas, c) : total;
+  w1 = c < ctas ? tree_cut(total, ctas, c + 1) : total;
+  if (w0 < w1 && w0 >= at && w0 < at + own) {
+    for (int b = lo;; ++b) {
+      const long long w = TreeSeq(a, b).work(a.Hkv);
+      if (w0 < at + w) {
+        st.b = b;
+        st.off = w0 - at;
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+}
+
+// The part of a unit that one CTA works on: tiles [t0, t1) of `tiles`.
+struct TreeSeg {
+  int b, kvh, rg, n, live, tiles, t0, t1, slot;
+  bool two;  // more than 128 rows
+  __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// A CTA's segments in order; every role walks them by itself.
+struct TreeWalk {
+  TreeSeq s;
+  int b, u, t, c;
+  long long left;
+  bool first;
+  __device__ TreeWalk(const TreeAttnArgs& a, int c_, int b0, long long off, long long count) {
+    b = b0;
+    c = c_;
+    left = count;
+    first = true;
+    if (left > 0) {
+      s = TreeSeq(a, b);
+      u = (int)(off / s.tiles);
+      t = (int)(off - (long long)u * s.tiles);
+    }
+  }
+  __device__ bool next(const TreeAttnArgs& a, TreeSeg& g) {
+    if (left <= 0) return false;
+    while (u >= s.groups * a.Hkv) {
+      s = TreeSeq(a, ++b);
+      u = 0;
+    }
+    const int cnt = (int)min(left, (long long)(s.tiles - t));
+    g.b = b;
+    g.kvh = u / s.groups;
+    g.rg = u - g.kvh * s.groups;
+    g.n = s.n;
+    g.live = s.live;
+    g.tiles = s.tiles;
+    g.t0 = t;
+    g.t1 = t + cnt;
+    g.two = s.live * a.G - g.rg * kTreeRows > 128;
+    g.slot = 2 * c + (first && t > 0 ? 0 : 1);
+    first = false;
+    left -= cnt;
+    t += cnt;
+    if (t == s.tiles) {
+      t = 0;
+      ++u;
+    }
+    return true;
+  }
+};
+
+// ---- TMEM helpers of this kernel -----------------------------------------------------------
+
+// 128 consecutive columns of 32 lanes into registers (thread t of the warp reads lane base + t): four loads of 32
+// columns in flight, one wait.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]),
+        "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]),
+        "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]),
+        "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]),
+        "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]),
+        "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]),
+        "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]),
+        "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+        "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]),
+        "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 registers into 32 consecutive columns, without waiting (tmem_wait_st follows).
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Registers of the calling warpgroup (all of its warps call it).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values along k in each 32-bit column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t tree_pack(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-    ((__nv_bfloat16*)a.out)[at] = hi;
-    if (a.out_type == ORTHRUS_BF16_PLANES)
-      ((__nv_bfloat16*)a.out)[a.out_lo + at] = __float2bfloat16_rn(x - __bfloat162float(hi));
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
-// One warp per row, one key at a time: the lanes hold d / 32 dims each.
-template <int D>
-__global__ void __launch_bounds__(128) tree_attention_kernel(const TreeAttnArgs a) {
+template <bool BF16>
+__device__ __forceinline__ bool tree_finite(uint32_t bits) {  // both 16-bit values
+  constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+  return (bits & e) != e && (bits >> 16 & e) != e;
+}
+
+// values out[at .. at + 8) of one row
+__device__ __forceinline__ void tree_store8(const TreeAttnArgs& a, size_t at, const float* x) {
+  if (a.out_type == ORTHRUS_BF16_PLANES) {
+    __nv_bfloat16* o = (__nv_bfloat16*)a.out + at;
+    st_split_x8(o, o + a.out_lo, x);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = a.out_type == ORTHRUS_BF16 ? tree_pack<true>(x[2 * i], x[2 * i + 1]) : tree_pack<false>(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>((uint16_t*)a.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// element offset of a unit's row in out
+__device__ __forceinline__ size_t tree_out_at(const TreeAttnArgs& a, int b, int kvh, int row) {
+  const int node = row / a.G;
+  return (((size_t)b * a.N + node) * a.Hkv * a.G + (size_t)kvh * a.G + (row - node * a.G)) * a.d;
+}
+
+// ---- the kernel -------------------------------------------------------------------------------
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKb,
+                          const __grid_constant__ CUtensorMap tmVb, const TreeAttnArgs a) {
+  using S = TreeSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem + S::kQ;
+  uint8_t* ring = smem + S::kRing;
+  TreeMisc& ms = *reinterpret_cast<TreeMisc*>(smem + S::kMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kHalves = D / 64;
+  constexpr int kHalf = kTreeKeys * 128;  // bytes of 64 columns of a tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&ms.full[s], 1);
+      mbar_init(&ms.empty[s], 1);
+    }
+    mbar_init(&ms.q_full, 1);
+    mbar_init(&ms.q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ms.s_full[s], 1);
+      mbar_init(&ms.p_full[s], 4);
+      mbar_init(&ms.o_done[s], 1);
+    }
+    mbar_init(&ms.done, 1);
+    ms.bad_any = 0;
+    for (int i = 0; i < 8; ++i) ms.bad[i] = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kTreeMmaWarp) {
+    tmem_alloc(&ms.tmem, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();  // lengths, masks, q and K/V come from earlier kernels
+  griddep_launch();
+  long long total, w0, w1;
+  int ctas;
+  tc_fence_before();
+  tree_start<kTreeThreads>(a, ms.start, blockIdx.x, gridDim.x, blockIdx.x == 0, total, ctas, w0, w1);
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  TreeWalk walk(a, blockIdx.x, ms.start.b, ms.start.off, w1 - w0);
+  TreeSeg g;
+
+  if (warp >= 8) {
+    regs_dec<kTreeRegsOther>();
+    if (warp == kTreeLoadWarp) {
+      // ---- loads: Q of a segment, then K and V of its tiles, through one ring ----
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        uint32_t it = 0, seg = 0;
+        bool ok = true;
+        while (ok && walk.next(a, g)) {
+          const int z = g.b * a.Hkv + g.kvh;
+          const int qtiles = g.two ? 2 : 1;
+          if (seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&ms.q_full, qtiles * S::kTile);
+          const int qrow = z * a.N * a.G + g.rg * kTreeRows;
+          for (int h = 0; h < qtiles; ++h)
+            for (int e = 0; e < kHalves; ++e)
+              tma_load_2d(sQ + h * S::kTile + e * kHalf, &tmQ, &ms.q_full, e * 64, qrow + h * 128);
+          ++seg;
+          const int ct = (g.n + kTreeKeys - 1) / kTreeKeys;
+          for (int t = g.t0; ok && t < g.t1; ++t) {
+            const bool blk = t >= ct;
+            const int y = (blk ? t - ct : t) * kTreeKeys;
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+              const uint32_t s = it % S::kStages, use = it / S::kStages;
+              if (use > 0 && !mbar_wait(&ms.empty[s], (use - 1) & 1, a.status)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(&ms.full[s], S::kTile);
+              const CUtensorMap* m = kv == 0 ? (blk ? &tmKb : &tmK) : (blk ? &tmVb : &tmV);
+              for (int e = 0; e < kHalves; ++e) tma_load_3d(ring + s * S::kTile + e * kHalf, m, &ms.full[s], e * 64, y, z);
+            }
+          }
+        }
+        // copies in flight land before the CTA ends
+        if (seg > 0) mbar_wait(&ms.q_full, (seg - 1) & 1, a.status);
+        for (uint32_t k = it > (uint32_t)S::kStages ? it - S::kStages : 0; k < it; ++k)
+          mbar_wait(&ms.full[k % S::kStages], (k / S::kStages) & 1, a.status);
+      }
+    } else if (warp == kTreeMmaWarp) {
+      // ---- products: S = Q K^T, O += P V; stream j & 1 takes job j ----
+      if (lane == 0) {
+        const uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
+        const uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
+        const uint32_t qa = smem_u32(sQ), ra = smem_u32(ring);
+        uint32_t base = 0, seg = 0, cnt[2] = {0, 0};  // ring position of the segment; jobs of each stream
+        bool ok = true;
+        while (ok && walk.next(a, g)) {
+          const int nt = g.t1 - g.t0;
+          const int jobs = g.two ? 2 * nt : nt;
+          ok = mbar_wait(&ms.q_full, seg & 1, a.status);
+          auto scores = [&](int j) {
+            const int k = g.two ? j >> 1 : j, st = j & 1;
+            const uint32_t pos = base + 2 * k, s = pos % S::kStages;
+            if (!(g.two && st) && !mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status)) return false;
+            tc_fence_after();
+            const uint32_t q = qa + (g.two ? st * S::kTile : 0), kk = ra + s * S::kTile;
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t off = (i >> 2) * kHalf + (i & 3) * 32;
+              mma_ss(tmem + st * 128, sw128_desc(q + off, 16, 1024), sw128_desc(kk + off, 16, 1024), idS, i > 0 ? 1u : 0u);
+            }
+            mma_commit(&ms.s_full[st]);
+            if (!g.two || st) mma_commit(&ms.empty[s]);
+            if (j == jobs - 1) mma_commit(&ms.q_empty);
+            return true;
+          };
+          for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
+          for (int j = 0; ok && j < jobs; ++j) {
+            const int k = g.two ? j >> 1 : j, st = j & 1;
+            const uint32_t pos = base + 2 * k + 1, s = pos % S::kStages;
+            ok = mbar_wait(&ms.p_full[st], cnt[st] & 1, a.status);
+            if (ok && !(g.two && st)) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t va = ra + s * S::kTile;
+            const bool fresh = g.two ? k == 0 : j < 2;  // the stream's first job of the segment
+            for (int i = 0; i < kTreeKeys / 16; ++i)
+              mma_ts(tmem + 256 + st * 128, tmem + st * 128 + i * 8, sw128_desc(va + i * 2048, kHalf, 1024), idO,
+                     fresh && i == 0 ? 0u : 1u);
+            mma_commit(&ms.o_done[st]);
+            if (!g.two || st) mma_commit(&ms.empty[s]);
+            ++cnt[st];
+            if (j + 2 < jobs) ok = scores(j + 2);
+          }
+          base += 2 * nt;
+          ++seg;
+        }
+        mma_commit(&ms.done);
+        mbar_wait(&ms.done, 0, a.status);
+      }
+    }
+  } else {
+    regs_inc<kTreeRegs>();
+    // ---- softmax: stream 0 or 1, thread = row ----
+    const int st = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256;
+    const float sl = a.scale_log2;
+    uint32_t base = 0, cnt = 0;
+    bool ok = true;  // after a wait that ran out: no more TMEM accesses, but the same barriers
+    while (walk.next(a, g)) {
+      const int nt = g.t1 - g.t0, ct = (g.n + kTreeKeys - 1) / kTreeKeys;
+      const int unit_rows = g.live * a.G - g.rg * kTreeRows;           // rows from this group on
+      const int lrow = (g.two ? st * 128 : 0) + r;                     // row within the group
+      const bool row_ok = lrow < unit_rows;
+      const bool warp_ok = lrow - lane < unit_rows;                    // the warp has a row
+      const int row = g.rg * kTreeRows + lrow;
+      const unsigned long long* words = a.mask + ((size_t)g.b * a.N + (row_ok ? row / a.G : 0)) * a.words;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int k = g.two ? 0 : st; k < nt; k += g.two ? 1 : 2) {
+        const int t = g.t0 + k, bt = t - ct;
+        const bool blk = t >= ct;
+        const int lim = blk ? g.live - bt * kTreeKeys : g.n - t * kTreeKeys;  // keys of the tile, if below 128
+        if (ok) ok = mbar_wait(&ms.s_full[st], cnt & 1, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && warp_ok) {
+          tc_fence_after();
+          float v[128];
+          tmem_ld128(tS, v);
+          if (blk || lim < kTreeKeys) {
+            uint32_t see[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int left = lim - 32 * q;
+              see[q] = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
+            }
+            if (blk) {
+              const unsigned long long x = words[2 * bt], y = 2 * bt + 1 < a.words ? words[2 * bt + 1] : 0ull;
+              see[0] &= (uint32_t)x;
+              see[1] &= (uint32_t)(x >> 32);
+              see[2] &= (uint32_t)y;
+              see[3] &= (uint32_t)(y >> 32);
+            }
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (!(see[i >> 5] >> (i & 31) & 1u)) v[i] = -INFINITY;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+          if (first) {
+            m = mt;
+          } else {
+            const bool move = mt > m + kTreeSlack;
+            if (__any_sync(0xffffffffu, move)) {
+              // the stream's last product is complete before its sums are scaled
+              ok = __all_sync(0xffffffffu, mbar_wait(&ms.o_done[st], (cnt - 1) & 1, a.status));
+              if (ok) {
+                tc_fence_after();
+                const float f = move ? exp2f(m - mt) : 1.f;
+                l *= f;
+                if (move) m = mt;
+#pragma unroll 1
+                for (int e = 0; e < D; e += 32) {
+                  float o[32];
+                  tmem_ld32(tO + st * 128 + e, o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] *= f;
+                  tmem_st32(tO + st * 128 + e, o);
+                }
+              }
+            }
+          }
+          const float shift = m == -INFINITY ? 0.f : m - kTreeShift;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float p0 = fast_exp2(fmaf(v[h * 64 + 2 * i], sl, -shift));
+              const float p1 = fast_exp2(fmaf(v[h * 64 + 2 * i + 1], sl, -shift));
+              sum[(2 * i) & 3] += p0;
+              sum[(2 * i + 1) & 3] += p1;
+              pk[i] = tree_pack<BF16>(p0, p1);
+            }
+            tmem_put32(tS + h * 32, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        if ((blk || lim < kTreeKeys) && !(g.two && st)) {
+          // thread r looks after key r: V rows that nobody may see become zero, and values that are
+          // not finite leave the product
+          const uint32_t pos = base + 2 * k + 1, s = pos % S::kStages;
+          if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            uint8_t* vr = ring + s * S::kTile + r * 128;
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < kHalves; ++e)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                uint4* p = reinterpret_cast<uint4*>(vr + e * kHalf + q * 16);
+                if (r >= lim) {
+                  *p = make_uint4(0u, 0u, 0u, 0u);
+                } else if (blk) {
+                  const uint4 x = *p;
+                  if (!(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
+                        tree_finite<BF16>(x.w))) {
+                    bad = true;
+                    uint16_t* half = reinterpret_cast<uint16_t*>(p);
+                    for (int i = 0; i < 8; ++i)
+                      if (!tree_finite<BF16>(half[i])) half[i] = 0;
+                  }
+                }
+              }
+            if (bad) {
+              const int j = bt * kTreeKeys + r;
+              atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
+              ms.bad_any = 1;
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&ms.p_full[st]);
+        first = false;
+        ++cnt;
+      }
+      base += 2 * nt;
+
+      // ---- the segment's sums ----
+      const bool mine = g.two || nt > st;  // this stream had a job
+      if (ok && mine) ok = mbar_wait(&ms.o_done[st], (cnt - 1) & 1, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      float w_own = 1.f, w_other = 0.f;
+      int e0 = 0, e1 = D;
+      if (!g.two) {
+        // both streams hold sums of the same rows: each joins one half of the columns
+        if (st) ms.ml[r] = make_float2(m, l);
+        named_bar_sync(1, 256);
+        const float2 ml1 = ms.ml[r];
+        named_bar_sync(2, 256);
+        if (!st) ms.ml[r] = make_float2(m, l);
+        named_bar_sync(1, 256);
+        const float2 ml0 = ms.ml[r];
+        const float top = fmaxf(ml0.x, ml1.x), ref = top == -INFINITY ? 0.f : top;
+        w_own = exp2f(ml0.x - ref);
+        w_other = exp2f(ml1.x - ref);
+        m = top;
+        l = ml0.y * w_own + ml1.y * w_other;
+        e0 = st ? D / 2 : 0;
+        e1 = st ? D : D / 2;
+      }
+      bool bad = *(volatile int*)&ms.bad_any != 0;
+      if (ok && warp_ok) {
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool whole = g.whole();
+        const size_t at = row_ok ? tree_out_at(a, g.b, g.kvh, row) : 0;
+        float4* po = a.part_o + (size_t)g.slot * (D / 4) * kTreeRows + lrow;
+#pragma unroll 1
+        for (int e = e0; e < e1; e += 32) {
+          float o[32];
+          if (g.two) {
+            tmem_ld32(tO + st * 128 + e, o);
+          } else {
+            tmem_ld32(tO + e, o);
+            if (nt > 1) {
+              float x[32];
+              tmem_ld32(tO + 128 + e, x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = o[i] * w_own + x[i] * w_other;
+            }
+          }
+          if (bad && row_ok) {
+            for (int j = 0; j < g.live; ++j)
+              if ((ms.bad[j >> 5] >> (j & 31) & 1u) && (words[j >> 6] >> (j & 63) & 1ull)) {
+                const size_t vat = ((size_t)(g.b * a.Hkv + g.kvh) * a.blk_stride + j) * D + e;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float x = BF16 ? __bfloat162float(((const __nv_bfloat16*)a.v_blk)[vat + i])
+                                       : __half2float(((const __half*)a.v_blk)[vat + i]);
+                  if (!isfinite(x)) o[i] += x;
+                }
+              }
+          }
+          if (!row_ok) continue;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) tree_store8(a, at + e + i, o + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              po[(size_t)(e / 4 + i) * kTreeRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (!whole && row_ok && (g.two || !st)) a.part_ml[(size_t)g.slot * kTreeRows + lrow] = make_float2(m, l);
+      }
+      tc_fence_before();
+      bad = named_bar_or(2, 256, bad);  // O and the marks are read before the next segment writes them
+      if (bad) {
+        if (threadIdx.x < 8) ms.bad[threadIdx.x] = 0u;
+        if (threadIdx.x == 0) ms.bad_any = 0;
+        named_bar_sync(1, 256);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTreeMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- joining the parts of a cut unit ---------------------------------------------------------
+
+// CTA x looks at the start of range x: where that cuts a unit, and is the first cut of it, the
+// CTA joins 32 rows x 32 columns of the unit, thread = (row, 4 columns). Parts are added in
+// key order: out = sum_c w_c O_c / sum_c w_c l_c, w_c = 2^(m_c - max m).
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a, int sms) {
+  __shared__ TreeStart start;
   griddep_wait();
   griddep_launch();
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const long long rows = (long long)a.B * a.Hkv * a.N * a.G;
-  if (row >= rows) return;
-  const int g = (int)(row % a.G), i = (int)(row / a.G % a.N), z = (int)(row / ((long long)a.G * a.N));
-  const int b = z / a.Hkv, kvh = z - b * a.Hkv;
-  int n = a.len[b];
-  if (n < 0 || n > a.cap) {
-    if (lane == 0) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
-    n = min(max(n, 0), a.cap);
+  const int c = blockIdx.x + 1;
+  long long total, w0, w1;
+  int ctas;
+  tree_start<kJoinThreads>(a, start, c, sms, false, total, ctas, w0, w1);
+  const int b = start.b;
+  if (b < 0) return;
+  const TreeSeq s(a, b);
+  const int u = (int)(start.off / s.tiles), t = (int)(start.off - (long long)u * s.tiles);
+  const long long g0 = w0 - t, g1 = g0 + s.tiles;
+  if (t == 0 || tree_cut(total, ctas, c - 1) > g0) return;  // no cut, or not the unit's first
+  const int kvh = u / s.groups, rg = u - kvh * s.groups;
+  const int c0 = c - 1;
+  int c1 = c;
+  while (c1 + 1 < ctas && tree_cut(total, ctas, c1 + 1) < g1) ++c1;
+  const int lrow = blockIdx.y * 32 + (threadIdx.x & 31);
+  if (rg * kTreeRows + lrow >= s.live * a.G) return;
+  const int e4 = blockIdx.z * 8 + (threadIdx.x >> 5);
+  // slot of part i: a range that starts inside the unit uses its CTA's first slot
+  auto slot = [&](int i) { return (size_t)(2 * i + (i == c0 ? 1 : 0)); };
+  float top = -INFINITY;
+  for (int i = c0; i <= c1; ++i) top = fmaxf(top, __ldcg(&a.part_ml[slot(i) * kTreeRows + lrow]).x);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = c0; i <= c1; ++i) {
+    const float2 ml = __ldcg(&a.part_ml[slot(i) * kTreeRows + lrow]);
+    const float4 x = __ldcg(&a.part_o[(slot(i) * (a.d / 4) + e4) * kTreeRows + lrow]);
+    const float w = exp2f(ml.x - ref);
+    l += ml.y * w;
+    o.x += x.x * w;
+    o.y += x.y * w;
+    o.z += x.z * w;
+    o.w += x.w * w;
   }
-  const int live = a.n_nodes ? min(max(a.n_nodes[b], 0), a.N) : a.N;
-  if (i >= live) return;
-  auto value = [&](const void* p, size_t at) {
-    return a.bf16 ? __bfloat162float(((const __nv_bfloat16*)p)[at]) : __half2float(((const __half*)p)[at]);
-  };
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = value(a.q, (size_t)row * D + lane + 32 * e);
-  auto step = [&](const void* kp, const void* vp, size_t at) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * value(kp, at + lane + 32 * e);
-    s = warp_sum(s) * a.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float f = mn == -INFINITY ? 1.f : exp2f(m - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * value(vp, at + lane + 32 * e);
-    m = mn;
-  };
-  for (int j = 0; j < n; ++j) step(a.k_cache, a.v_cache, ((size_t)z * a.cap + j) * D);
-  const unsigned long long* words = a.mask + ((size_t)b * a.N + i) * a.words;
-  for (int j = 0; j < live; ++j)
-    if ((words[j >> 6] >> (j & 63)) & 1ull) step(a.k_blk, a.v_blk, ((size_t)z * a.blk_stride + j) * D);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t at = (((size_t)b * a.N + i) * a.Hkv * a.G + (size_t)kvh * a.G + g) * D;
-#pragma unroll
-  for (int e = 0; e < E; ++e) tree_store(a, at + lane + 32 * e, o[e] * inv);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t to = tree_out_at(a, b, kvh, rg * kTreeRows + lrow) + e4 * 4;
+  const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  if (a.out_type == ORTHRUS_FP16) {
+    *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(tree_pack<false>(y[0], y[1]), tree_pack<false>(y[2], y[3]));
+  } else if (a.out_type == ORTHRUS_BF16) {
+    *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(tree_pack<true>(y[0], y[1]), tree_pack<true>(y[2], y[3]));
+  } else {
+    uint32_t h0, h1, l0, l1;
+    split_bf16x2(y[0], y[1], h0, l0);
+    split_bf16x2(y[2], y[3], h1, l1);
+    *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2*>((uint16_t*)a.out + a.out_lo + to) = make_uint2(l0, l1);
+  }
 }
 
 }  // namespace orthrus

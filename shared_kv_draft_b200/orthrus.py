@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
+import struct
 from builtins import len as _length  # some calls below have an argument `len`, the cache lengths
 
 import numpy as np
@@ -260,25 +261,28 @@ def linear_workspace_bytes(M, N, Kd) -> int:
 _TYPES = {torch.float32: FP32, torch.bfloat16: BF16, torch.float16: FP16}
 
 
-class _Call:
-    """The stream a call runs on: `stream`, or the current stream of the device that holds its
-    tensors, which is made the current device for the call where it is another one."""
+_PART = struct.Struct("PPiiiiiiqqqqqqq")  # orthrus_rotary_part
+assert _PART.size == C.sizeof(RotaryPart)
 
-    def __init__(self, device, stream):
-        self.index = device.index
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.back = None
 
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.index != now:
-            self.back = now
-            torch.cuda.set_device(self.index)
-        return self.stream.cuda_stream
+def _on(dev, stream):
+    """The raw stream of a call on device `dev`: `stream`, or the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+
+def _call(dev, fn, *args):
+    """fn(*args) with `dev`, the device of the call's tensors, as the current device."""
+    now = torch._C._cuda_getDevice()
+    if now == dev:
+        code = fn(*args)
+    else:
+        torch.cuda.set_device(dev)
+        try:
+            code = fn(*args)
+        finally:
+            torch.cuda.set_device(now)
+    if code != OK:
+        raise OrthrusError(fn.__name__, code)
 
 
 def _arg(ok, call, what):
@@ -286,26 +290,41 @@ def _arg(ok, call, what):
         raise ValueError(f"{call}: {what}")
 
 
-def _dense(call, device, dtype, **tensors):
-    """Every given tensor lies densely on `device` with `dtype` (None passes where it is optional)."""
-    for name, t in tensors.items():
-        _arg(t is None or (t.dtype is dtype and t.device == device and t.is_contiguous()), call,
-             f"{name} must be a contiguous {dtype} tensor on {device}")
+def _dense(call, dev, dtype, shape, names, *tensors):
+    """Every given tensor lies densely on device `dev`, with this dtype and shape (None: any)."""
+    for i, t in enumerate(tensors):
+        if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            raise ValueError(f"{call}: {names.split()[i]} must be a contiguous {dtype} tensor on device {dev}"
+                             + ("" if shape is None else f" of shape {tuple(shape)}"))
+
+
+def _batch_ints(call, dev, B, names, *tensors):
+    """int32 [batch] arrays, None where they are optional; their addresses."""
+    out = []
+    for i, t in enumerate(tensors):
+        if t is None:
+            out.append(None)
+            continue
+        if not (t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous() and t.numel() == B):
+            raise ValueError(f"{call}: {names.split()[i]} must be int32 [{B}] on device {dev}")
+        out.append(t.data_ptr())
+    return out
 
 
 def tree_layout(parents, depth, mask, n_nodes=None, status=None, stream=None):
     """Depths and visibility words of draft trees. parents: int32 [B][N]; depth: int32 [B][N]; mask:
     int64 [B][N][ceil(N / 64)] (the words' bits)."""
-    dev, name = parents.device, "tree_layout"
-    _arg(parents.dim() == 2 and parents.is_cuda, name, "parents must be [batch][nodes] on a GPU")
-    B, N = parents.shape
-    _dense(name, dev, torch.int32, parents=parents, depth=depth, n_nodes=n_nodes, status=status)
-    _dense(name, dev, torch.int64, mask=mask)
-    _arg(depth.shape == parents.shape and mask.shape == (B, N, (N + 63) // 64), name, "depth or mask has another shape")
-    _arg(n_nodes is None or n_nodes.shape == (B,), name, "n_nodes must be [batch]")
-    with _Call(dev, stream) as st:
-        code = load().orthrus_tree_layout(_ptr(parents), _ptr(n_nodes), B, N, _ptr(depth), _ptr(mask), _ptr(status), st)
-    _check("orthrus_tree_layout", code)
+    dev, name = parents.get_device(), "tree_layout"
+    shape = parents.shape
+    _arg(dev >= 0 and _length(shape) == 2, name, "parents must be [batch][nodes] on a GPU")
+    B, N = shape
+    _dense(name, dev, torch.int32, shape, "parents depth", parents, depth)
+    _dense(name, dev, torch.int64, (B, N, (N + 63) // 64), "mask", mask)
+    nn, = _batch_ints(name, dev, B, "n_nodes", n_nodes)
+    st, = _batch_ints(name, dev, 1, "status", status)
+    _call(dev, load().orthrus_tree_layout, parents.data_ptr(), nn, B, N, depth.data_ptr(), mask.data_ptr(), st,
+          _on(dev, stream))
 
 
 def tree_attention_workspace_bytes(batch, n_kv_heads, group, nodes, head_dim) -> int:
@@ -317,35 +336,32 @@ def tree_attention(q, k_cache, v_cache, k_blk, v_blk, len, mask, out, workspace,
     """Attention of draft trees over one layer's cache. q: [B][Hkv][N*G][d]; k_cache, v_cache:
     [B][Hkv][capacity][d]; k_blk, v_blk: [B][Hkv][>= N][d], all fp16 or all bf16; len: int32 [B]; mask: int64
     [B][N][words]; out: fp16 or bf16 [B*N][H*d], or bf16 [2][B*N][H*d] (hi and lo plane); workspace:
-    uint8, tree_attention_workspace_bytes() or more."""
-    dev, t, name = q.device, q.dtype, "tree_attention"
-    _arg(q.dim() == 4 and q.is_cuda and t in (torch.float16, torch.bfloat16), name,
+    tree_attention_workspace_bytes() or more."""
+    dev, t, name = q.get_device(), q.dtype, "tree_attention"
+    _arg(dev >= 0 and q.dim() == 4 and (t is torch.float16 or t is torch.bfloat16), name,
          "q must be fp16 or bf16 [batch][kv heads][nodes*group][d] on a GPU")
     B, H, R, d = q.shape
-    _dense(name, dev, t, q=q, k_cache=k_cache, v_cache=v_cache, k_blk=k_blk, v_blk=v_blk)
-    _arg(mask.dim() == 3 and mask.shape[0] == B and mask.shape[1] > 0, name, "mask must be [batch][nodes][words]")
-    N = mask.shape[1]
-    _dense(name, dev, torch.int64, mask=mask)
-    _arg(mask.shape[2] == (N + 63) // 64 and R % N == 0, name, "mask does not fit q")
-    _dense(name, dev, torch.int32, len=len, n_nodes=n_nodes, status=status)
-    _arg(len.shape == (B,) and (n_nodes is None or n_nodes.shape == (B,)), name, "len and n_nodes must be [batch]")
-    for c, least in ((k_cache, 1), (k_blk, N)):
-        _arg(c.dim() == 4 and c.shape[:2] == (B, H) and c.shape[2] >= least and c.shape[3] == d, name,
-             "a cache or block has another shape")
-    _arg(v_cache.shape == k_cache.shape and v_blk.shape == k_blk.shape, name, "K and V must have one shape")
-    planes = out.dim() == 3
-    _arg(out.shape == ((2, B * N, H * (R // N) * d) if planes else (B * N, H * (R // N) * d))
-         and (out.dtype is torch.bfloat16 or (out.dtype is torch.float16 and not planes)), name,
-         "out must be [batch*nodes][heads*d] in fp16 or bf16, or two such planes in bf16")
-    _dense(name, dev, out.dtype, out=out)
-    _dense(name, dev, workspace.dtype, workspace=workspace)
-    with _Call(dev, stream) as st:
-        code = load().orthrus_tree_attention(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_blk.data_ptr(), v_blk.data_ptr(), len.data_ptr(),
-            _ptr(n_nodes), mask.data_ptr(), B, H, R // N, N, d, k_cache.shape[2], k_blk.shape[2], _TYPES[t],
-            BF16_PLANES if planes else _TYPES[out.dtype], scale, out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _ptr(status), st)
-    _check("orthrus_tree_attention", code)
+    _arg(mask.dim() == 3 and mask.size(1) > 0, name, "mask must be [batch][nodes][words]")
+    N = mask.size(1)
+    G = R // N
+    _arg(G * N == R, name, "mask does not fit q")
+    _arg(k_cache.dim() == 4 and k_blk.dim() == 4 and k_blk.size(2) >= N, name, "a cache or block has another shape")
+    cap, rows = k_cache.size(2), k_blk.size(2)
+    _dense(name, dev, t, None, "q", q)
+    _dense(name, dev, t, (B, H, cap, d), "k_cache v_cache", k_cache, v_cache)
+    _dense(name, dev, t, (B, H, rows, d), "k_blk v_blk", k_blk, v_blk)
+    _dense(name, dev, torch.int64, (B, N, (N + 63) // 64), "mask", mask)
+    _arg(len is not None, name, "len must be given")
+    ln, nn = _batch_ints(name, dev, B, "len n_nodes", len, n_nodes)
+    st, = _batch_ints(name, dev, 1, "status", status)
+    planes, to = out.dim() == 3, out.dtype
+    _arg(to is torch.bfloat16 or (to is torch.float16 and not planes), name, "out must be fp16 or bf16, planes bf16")
+    _dense(name, dev, to, (2, B * N, H * G * d) if planes else (B * N, H * G * d), "out", out)
+    _dense(name, dev, workspace.dtype, None, "workspace", workspace)
+    _call(dev, load().orthrus_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_blk.data_ptr(),
+          v_blk.data_ptr(), ln, nn, mask.data_ptr(), B, H, G, N, d, cap, rows, _TYPES[t],
+          BF16_PLANES if planes else _TYPES[to], scale, out.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), st, _on(dev, stream))
 
 
 def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, new_len, pending, accept_len, path,
@@ -353,29 +369,27 @@ def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, ne
     """Greedy consensus on draft trees and the accepted paths' K/V rows into the cache. k_blk, v_blk:
     [L][B][Hkv][>= N][d] and k_cache, v_cache: [L][B][Hkv][capacity][d] of one 16-bit type; the others int32, [B] or
     [B][N]. new_len may be len."""
-    dev, name = parents.device, "tree_commit"
-    _arg(parents.dim() == 2 and parents.is_cuda, name, "parents must be [batch][nodes] on a GPU")
-    B, N = parents.shape
-    _dense(name, dev, torch.int32, parents=parents, tokens=tokens, argmax=argmax, path=path, committed=committed, len=len,
-           new_len=new_len, pending=pending, accept_len=accept_len, n_nodes=n_nodes, status=status)
-    for t in (tokens, argmax, path, committed):
-        _arg(t.shape == (B, N), name, "tokens, argmax, path and committed must be [batch][nodes]")
-    for t in (len, new_len, pending, accept_len, n_nodes):
-        _arg(t is None or t.shape == (B,), name, "len, new_len, pending, accept_len and n_nodes must be [batch]")
-    _arg(k_cache.dim() == 5 and k_blk.dim() == 5 and k_cache.element_size() == 2, name,
+    dev, name = parents.get_device(), "tree_commit"
+    shape = parents.shape
+    _arg(dev >= 0 and _length(shape) == 2, name, "parents must be [batch][nodes] on a GPU")
+    B, N = shape
+    _dense(name, dev, torch.int32, shape, "parents tokens argmax path committed", parents, tokens, argmax, path, committed)
+    for x in (len, new_len, pending, accept_len):
+        _arg(x is not None, name, "len, new_len, pending and accept_len must be given")
+    ln, nl, pend, acc, nn = _batch_ints(name, dev, B, "len new_len pending accept_len n_nodes", len, new_len, pending,
+                                        accept_len, n_nodes)
+    st, = _batch_ints(name, dev, 1, "status", status)
+    t = k_cache.dtype
+    _arg(k_cache.dim() == 5 and k_blk.dim() == 5 and t.itemsize == 2, name,
          "caches and blocks must be five-dimensional with 16-bit elements")
     L, _, H, cap, d = k_cache.shape
-    _dense(name, dev, k_cache.dtype, k_blk=k_blk, v_blk=v_blk, k_cache=k_cache, v_cache=v_cache)
-    _arg(k_cache.shape == v_cache.shape and k_blk.shape == v_blk.shape and k_cache.shape[1] == B
-         and k_blk.shape[:3] == (L, B, H) and k_blk.shape[3] >= N and k_blk.shape[4] == d, name,
-         "a cache or block has another shape")
-    with _Call(dev, stream) as st:
-        code = load().orthrus_tree_commit(
-            parents.data_ptr(), tokens.data_ptr(), argmax.data_ptr(), _ptr(n_nodes), k_blk.data_ptr(), v_blk.data_ptr(),
-            k_blk.shape[3], k_cache.data_ptr(), v_cache.data_ptr(), L, B, H, cap, d, N, len.data_ptr(),
-            new_len.data_ptr(), pending.data_ptr(), accept_len.data_ptr(), path.data_ptr(), committed.data_ptr(),
-            _ptr(status), st)
-    _check("orthrus_tree_commit", code)
+    rows = k_blk.size(3)
+    _arg(rows >= N, name, "k_blk and v_blk must hold a row for every node")
+    _dense(name, dev, t, (L, B, H, cap, d), "k_cache v_cache", k_cache, v_cache)
+    _dense(name, dev, t, (L, B, H, rows, d), "k_blk v_blk", k_blk, v_blk)
+    _call(dev, load().orthrus_tree_commit, parents.data_ptr(), tokens.data_ptr(), argmax.data_ptr(), nn, k_blk.data_ptr(),
+          v_blk.data_ptr(), rows, k_cache.data_ptr(), v_cache.data_ptr(), L, B, H, cap, d, N, ln, nl, pend, acc,
+          path.data_ptr(), committed.data_ptr(), st, _on(dev, stream))
 
 
 @functools.lru_cache(maxsize=64)
@@ -398,38 +412,33 @@ def rotary(rope, parts, len=None, offsets=None, inverse=False, status=None, stre
     [B][rows][kv heads][group][d]; views with any strides, the last dimension dense; fp32, bf16 or fp16.
     rows = T, or with ROTARY_APPEND the rows of the cache that rows len[b] + t are written to. ROTARY_COPY:
     no rotation; ROTARY_BF16_VALUES: rounded to bf16 first. inverse: back by the same angles (the gradient)."""
-    name = "rotary"
-    n = _length(parts)
+    name, n, hd = "rotary", _length(parts), rope.head_dim
     _arg(1 <= n <= ROTARY_MAX_PARTS, name, f"1 to {ROTARY_MAX_PARTS} parts")
-    dev = parts[0][0].device
-    B, T = parts[0][0].shape[:2]
-    arr = (RotaryPart * n)()
-    for a, part in zip(arr, parts):
-        src, dst = part[0], part[1]
-        flags = part[2] if _length(part) > 2 else 0
-        _arg(src.is_cuda and src.device == dev and dst.device == dev, name, "all tensors must be on one GPU")
-        _arg(src.dtype in _TYPES and dst.dtype in _TYPES, name, "tensors must be fp32, bf16 or fp16")
-        ss, ds, shape = src.stride(), dst.stride(), dst.shape
-        _arg(src.dim() == 4 and src.shape[:2] == (B, T) and src.shape[3] == rope.head_dim and ss[3] == 1, name,
+    first = parts[0][0]
+    dev = first.get_device()
+    _arg(dev >= 0 and first.dim() == 4, name, "src must be [batch][tokens][heads][d] on a GPU")
+    B, T = first.size(0), first.size(1)
+    packed = b""
+    for src, dst, *flags in parts:
+        flags = flags[0] if flags else 0
+        ss, ds, sh, dh = src.stride(), dst.stride(), src.shape, dst.shape
+        _arg(src.get_device() == dev and dst.get_device() == dev and src.dtype in _TYPES and dst.dtype in _TYPES, name,
+             "tensors must be fp32, bf16 or fp16 on one GPU")
+        _arg(_length(sh) == 4 and sh[0] == B and sh[1] == T and sh[3] == hd and (ss[3] == 1), name,
              "src must be [batch][tokens][heads][d] with a dense last dimension")
-        heads = src.shape[2]
-        grouped = dst.dim() == 5
-        _arg((grouped or dst.dim() == 4) and shape[0] == B and shape[-1] == rope.head_dim and ds[-1] == 1
-             and (shape[2] * shape[3] if grouped else shape[2]) == heads
-             and (flags & ROTARY_APPEND or shape[1] == T), name,
+        heads, nd = sh[2], _length(dh)
+        group = dh[3] if nd == 5 else 1
+        _arg((nd == 4 or nd == 5) and dh[0] == B and dh[-1] == hd and ds[-1] == 1 and dh[2] * group == heads
+             and (flags & ROTARY_APPEND or dh[1] == T), name,
              "dst must be [batch][rows][heads][d] or [batch][rows][kv heads][group][d] with a dense last dimension")
-        a.src, a.dst, a.src_type, a.dst_type = src.data_ptr(), dst.data_ptr(), _TYPES[src.dtype], _TYPES[dst.dtype]
-        a.heads, a.group, a.flags, a.rows = heads, shape[3] if grouped else 1, flags, shape[1]
-        a.src_batch, a.src_token, a.src_head = ss[:3]
-        a.dst_batch, a.dst_token, a.dst_kv = ds[:3]
-        a.dst_head = ds[3] if grouped else 0
-    _dense(name, dev, torch.int32, len=len, offsets=offsets, status=status)
-    _arg((len is None or len.shape == (B,)) and (offsets is None or offsets.shape == (B, T)), name,
-         "len must be [batch] and offsets [batch][tokens]")
-    with _Call(dev, stream) as st:
-        code = load().orthrus_rotary(C.byref(rope), arr, n, B, T, _ptr(len), _ptr(offsets), int(bool(inverse)),
-                                     _ptr(status), st)
-    _check("orthrus_rotary", code)
+        packed += _PART.pack(src.data_ptr(), dst.data_ptr(), _TYPES[src.dtype], _TYPES[dst.dtype], heads, group, flags,
+                             dh[1], ss[0], ss[1], ss[2], ds[0], ds[1], ds[2], ds[3] if nd == 5 else 0)
+    ln, = _batch_ints(name, dev, B, "len", len)
+    st, = _batch_ints(name, dev, 1, "status", status)
+    if offsets is not None:
+        _dense(name, dev, torch.int32, (B, T), "offsets", offsets)
+    _call(dev, load().orthrus_rotary, C.addressof(rope), packed, n, B, T, ln, None if offsets is None else offsets.data_ptr(),
+          1 if inverse else 0, st, _on(dev, stream))
 
 
 # ---- a plan with its device buffers --------------------------------------------------------------
