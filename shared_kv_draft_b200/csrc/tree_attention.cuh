@@ -252,6 +252,17 @@ __device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// One thread of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Registers of the calling warpgroup (all of its warps call it).
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint8_t* sQ = smem + S::kQ;
   uint8_t* ring = smem + S::kRing;
   TreeMisc& ms = *reinterpret_cast<TreeMisc*>(smem + S::kMisc);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kHalves = D / 64;
   constexpr int kHalf = kTreeKeys * 128;  // bytes of 64 columns of a tile
 
@@ -404,56 +415,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           mbar_wait(&ms.full[k % S::kStages], (k / S::kStages) & 1, a.status);
       }
     } else if (warp == kTreeMmaWarp) {
-      // ---- products: S = Q K^T, O += P V; stream j & 1 takes job j ----
-      if (lane == 0) {
-        const uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
-        const uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
-        const uint32_t qa = smem_u32(sQ), ra = smem_u32(ring);
-        uint32_t base = 0, seg = 0, cnt[2] = {0, 0};  // ring position of the segment; jobs of each stream
-        bool ok = true;
-        while (ok && walk.next(a, g)) {
-          const int nt = g.t1 - g.t0;
-          const int jobs = g.two ? 2 * nt : nt;
-          ok = mbar_wait(&ms.q_full, seg & 1, a.status);
-          auto scores = [&](int j) {
-            const int k = g.two ? j >> 1 : j, st = j & 1;
-            const uint32_t pos = base + 2 * k, s = pos % S::kStages;
-            if (!(g.two && st) && !mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status)) return false;
-            tc_fence_after();
-            const uint32_t q = qa + (g.two ? st * S::kTile : 0), kk = ra + s * S::kTile;
+      // ---- products: S = Q K^T, O += P V; stream j & 1 takes job j. The whole warp runs the loop, one
+      // elected thread issues: descriptors stay in uniform registers ----
+      constexpr uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
+      constexpr uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
+      const bool issue = elect_one();
+      const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sw128_desc(smem_u32(ring), 16, 1024), v_desc = sw128_desc(smem_u32(ring), kHalf, 1024);
+      uint32_t base = 0, seg = 0, cnt[2] = {0, 0};  // ring position of the segment; jobs of each stream
+      bool ok = true;
+      while (ok && walk.next(a, g)) {
+        const int nt = g.t1 - g.t0;
+        const int jobs = g.two ? 2 * nt : nt;
+        ok = mbar_wait(&ms.q_full, seg & 1, a.status);
+        auto scores = [&](int j) {
+          const int k = g.two ? j >> 1 : j, st = j & 1;
+          const uint32_t pos = base + 2 * k, s = pos % S::kStages;
+          if (!(g.two && st) && !mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status)) return false;
+          tc_fence_after();
+          const uint64_t qd = q_desc + (g.two ? st * (S::kTile >> 4) : 0), kd = k_desc + s * (S::kTile >> 4);
+          const uint32_t to = tmem + st * 128;
+          if (issue) {
+#pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              const uint32_t off = (i >> 2) * kHalf + (i & 3) * 32;
-              mma_ss(tmem + st * 128, sw128_desc(q + off, 16, 1024), sw128_desc(kk + off, 16, 1024), idS, i > 0 ? 1u : 0u);
+              const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+              mma_ss(to, qd + off, kd + off, idS, i > 0 ? 1u : 0u);
             }
             mma_commit(&ms.s_full[st]);
             if (!g.two || st) mma_commit(&ms.empty[s]);
             if (j == jobs - 1) mma_commit(&ms.q_empty);
-            return true;
-          };
-          for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
-          for (int j = 0; ok && j < jobs; ++j) {
-            const int k = g.two ? j >> 1 : j, st = j & 1;
-            const uint32_t pos = base + 2 * k + 1, s = pos % S::kStages;
-            ok = mbar_wait(&ms.p_full[st], cnt[st] & 1, a.status);
-            if (ok && !(g.two && st)) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t va = ra + s * S::kTile;
-            const bool fresh = g.two ? k == 0 : j < 2;  // the stream's first job of the segment
-            for (int i = 0; i < kTreeKeys / 16; ++i)
-              mma_ts(tmem + 256 + st * 128, tmem + st * 128 + i * 8, sw128_desc(va + i * 2048, kHalf, 1024), idO,
-                     fresh && i == 0 ? 0u : 1u);
+          }
+          return true;
+        };
+        for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
+        for (int j = 0; ok && j < jobs; ++j) {
+          const int k = g.two ? j >> 1 : j, st = j & 1;
+          const uint32_t pos = base + 2 * k + 1, s = pos % S::kStages;
+          ok = mbar_wait(&ms.p_full[st], cnt[st] & 1, a.status);
+          if (ok && !(g.two && st)) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc + s * (S::kTile >> 4);
+          const uint32_t to = tmem + 256 + st * 128, from = tmem + st * 128;
+          const uint32_t add = (g.two ? k == 0 : j < 2) ? 0u : 1u;  // the stream's first job starts its sums
+          if (issue) {
+#pragma unroll
+            for (int i = 0; i < kTreeKeys / 16; ++i) mma_ts(to, from + i * 8, vd + i * (2048 >> 4), idO, i > 0 ? 1u : add);
             mma_commit(&ms.o_done[st]);
             if (!g.two || st) mma_commit(&ms.empty[s]);
-            ++cnt[st];
-            if (j + 2 < jobs) ok = scores(j + 2);
           }
-          base += 2 * nt;
-          ++seg;
+          ++cnt[st];
+          if (j + 2 < jobs) ok = scores(j + 2);
         }
-        mma_commit(&ms.done);
-        mbar_wait(&ms.done, 0, a.status);
+        base += 2 * nt;
+        ++seg;
       }
+      if (issue) mma_commit(&ms.done);
+      mbar_wait(&ms.done, 0, a.status);
     }
   } else {
     regs_inc<kTreeRegs>();
