@@ -16,7 +16,7 @@ bool orthrus::tree_sizes_ok(int batch, int nodes) {
 // Two parts for each CTA: of the unit in which its range starts, and of the one in which it ends.
 size_t orthrus::tree_attn_scratch(int B, int Hkv, int G, int nodes, int d) {
   (void)B, (void)Hkv, (void)G, (void)nodes;
-  return (size_t)2 * num_sms() * kTreeRows * ((size_t)d * 4 + 8);
+  return (size_t)2 * num_sms() * kTreeRows * ((size_t)d * 4 + 8) + (size_t)num_sms() * sizeof(int4);
 }
 
 namespace {
@@ -29,7 +29,7 @@ orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap
              m[3], m[4], a) != cudaSuccess)
     return ORTHRUS_ERR_CUDA;
   const int rows = std::min(kTreeRows, a.N * a.G);
-  return launch(tree_combine_kernel, dim3(sms - 1, (rows + 31) / 32, D / 32), dim3(kJoinThreads), 0, st, a, sms) ==
+  return launch(tree_combine_kernel, dim3(sms - 1, (rows + 31) / 32, D / 32), dim3(kJoinThreads), 0, st, a) ==
                  cudaSuccess
              ? ORTHRUS_OK
              : ORTHRUS_ERR_CUDA;
@@ -42,6 +42,11 @@ orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* wo
   TreeAttnArgs a = args;
   a.part_o = (float4*)workspace;
   a.part_ml = (float2*)(a.part_o + (size_t)2 * num_sms() * kTreeRows * (a.d / 4));
+  a.note = (int4*)(a.part_ml + (size_t)2 * num_sms() * kTreeRows);
+  // the line of tiles is counted in 31 bits
+  const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
+  const long long units = (long long)a.B * a.Hkv * (((long long)a.N * a.G + kTreeRows - 1) / kTreeRows);
+  if (units * tiles > INT32_MAX) return ORTHRUS_ERR_UNSUPPORTED;
   const CUtensorMapDataType dt = a.bf16 ? kBF16 : kF16;
   const uint64_t z = (uint64_t)a.B * a.Hkv;
   CUtensorMap m[5];

@@ -19,6 +19,7 @@ struct TreeAttnArgs {
   // scratch, laid out by launch_tree_attention
   float4* part_o;   // [2 per CTA][d / 4][256 rows]
   float2* part_ml;  // [2 per CTA][256 rows]: (reference, sum of weights)
+  int4* note;       // [CTAs]: (sequence, KV head, row group, last range) of a cut unit, or x < 0
 };
 
 // Embedding of a tree block: row m = b * nodes + i at position len[b] + depth[i]; node 0 is

@@ -44,35 +44,31 @@
 
 namespace orthrus {
 
-constexpr int kTreeThreads = 384;   // two softmax warpgroups; one with the load and the MMA warp
-// Registers a thread: 384 threads are launched with 168 each (64512); the softmax warps hold a row of
-// scores in registers and take 208, the others give theirs up: 256 x 208 + 128 x 88 = 64512.
-constexpr int kTreeRegs = 208, kTreeRegsOther = 88;
-constexpr int kTreeKeys = 128;      // keys of a tile
+constexpr int kTreeThreads = 384;  // 8 softmax warps, load, MMA and note warp, one idle
+constexpr int kTreeKeys = 64;      // keys of a tile: one visibility word
 constexpr int kTreeRows = 256;      // rows of a unit
 constexpr float kTreeSlack = 8.f;   // how far scores may exceed the reference (log2)
 constexpr float kTreeShift = 7.f;   // factor on the weights (log2)
-constexpr int kTreeLoadWarp = 8, kTreeMmaWarp = 9;
+constexpr int kTreeLoadWarp = 8, kTreeMmaWarp = 9, kTreeNoteWarp = 10;
 
 template <int D>
 struct TreeSmem {
-  static constexpr int kTile = kTreeKeys * D * 2;  // bytes of a K, V or Q tile
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kTile = kTreeKeys * D * 2;  // bytes of a K or V tile
+  static constexpr int kQTile = 128 * D * 2;       // of 128 rows of q
+  static constexpr int kStages = D == 128 ? 10 : 20;
   static constexpr int kQ = 0;
-  static constexpr int kRing = 2 * kTile;
+  static constexpr int kRing = 2 * kQTile;
   static constexpr int kMisc = kRing + kStages * kTile;
   static constexpr int kBytes = 1024 + kMisc + 2048;  // 1024: alignment of the dynamic part
 };
 
 struct TreeStart {  // where a CTA's range of tiles starts
-  long long scan[kTreeThreads / 32], off;
-  int b;
+  int scan[kTreeThreads / 32], b, off;
 };
 
 struct TreeMisc {
-  uint64_t full[10], empty[10], q_full, q_empty, s_full[2], p_full[2], o_done[2], done;
+  uint64_t full[20], empty[20], q_full, q_empty, s_full[4], p_full[4], o_done[2], done;  // s_full, p_full: 2 stream + buffer
   uint32_t tmem;
-  int ok[2];            // per stream: the last wait of its leader succeeded
   int bad_any;
   unsigned int bad[8];  // tree rows with values that are not finite (this segment)
   TreeStart start;
@@ -91,48 +87,56 @@ struct TreeSeq {
     groups = (live * a.G + kTreeRows - 1) / kTreeRows;
     tiles = (n + kTreeKeys - 1) / kTreeKeys + (live + kTreeKeys - 1) / kTreeKeys;
   }
-  __device__ long long work(int Hkv) const { return (long long)groups * Hkv * tiles; }
+  __device__ int work(int Hkv) const { return groups * Hkv * tiles; }
 };
 
-__device__ __forceinline__ long long tree_cut(long long total, int ctas, int c) { return total * c / ctas; }
+// The line of `total` tiles in `ctas` ranges whose lengths differ by at most one: start of range c.
+// (Tiles of all units fit 31 bits, which the host checks with the capacity.)
+struct TreeCut {
+  int total, ctas, each, more;
+  __device__ TreeCut(int total_, int sms) {
+    total = total_;
+    ctas = max(1, min(sms, total));
+    each = total / ctas;
+    more = total - each * ctas;
+  }
+  __device__ int at(int c) const { return min(total, c * each + min(c, more)); }
+};
 
 // Finds the start of range c of the line of tiles: sequence st.b and tile st.off among that
-// sequence's (st.b = -1 if the range is empty). Returns all tiles, the ranges and the bounds of
-// this one. Called by all THREADS threads of the CTA; the sums before each sequence are an
-// exclusive scan over the CTA, every thread holding a contiguous share of the sequences.
-template <int THREADS>
-__device__ __forceinline__ void tree_start(const TreeAttnArgs& a, TreeStart& st, int c, int sms, bool check,
-                                           long long& total, int& ctas, long long& w0, long long& w1) {
-  const int per = (a.B + THREADS - 1) / THREADS;
+// sequence's (st.b = -1 if the range is empty). Called by all threads of the CTA; the sums
+// before each sequence are an exclusive scan over the CTA, every thread holding a contiguous
+// share of the sequences.
+__device__ __forceinline__ TreeCut tree_start(const TreeAttnArgs& a, TreeStart& st, int c, int sms) {
+  const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
   const int lo = min(a.B, (int)threadIdx.x * per), hi = min(a.B, lo + per);
-  long long own = 0;
+  int own = 0;
   for (int b = lo; b < hi; ++b) {
     own += TreeSeq(a, b).work(a.Hkv);
     const int n = a.len[b];
-    if (check && (n < 0 || n > a.cap)) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
+    if (c == 0 && (n < 0 || n > a.cap)) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
   }
-  long long inc = own;
+  int inc = own;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
   if (lane == 31) st.scan[warp] = inc;
   if (threadIdx.x == 0) st.b = -1;
   __syncthreads();
-  long long at = inc - own;
-  total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
+  int at = inc - own, total = 0;
+#pragma unroll
+  for (int w = 0; w < kTreeThreads / 32; ++w) {
     if (w < warp) at += st.scan[w];
     total += st.scan[w];
   }
-  ctas = (int)max(1ll, min((long long)sms, total));
-  w0 = c < ctas ? tree_cut(total, ctas, c) : total;
-  w1 = c < ctas ? tree_cut(total, ctas, c + 1) : total;
-  if (w0 < w1 && w0 >= at && w0 < at + own) {
+  const TreeCut cut(total, sms);
+  const int w0 = cut.at(c);
+  if (w0 < total && w0 >= at && w0 < at + own) {
     for (int b = lo;; ++b) {
-      const long long w = TreeSeq(a, b).work(a.Hkv);
+      const int w = TreeSeq(a, b).work(a.Hkv);
       if (w0 < at + w) {
         st.b = b;
         st.off = w0 - at;
@@ -142,6 +146,7 @@ __device__ __forceinline__ void tree_start(const TreeAttnArgs& a, TreeStart& st,
     }
   }
   __syncthreads();
+  return cut;
 }
 
 // The part of a unit that one CTA works on: tiles [t0, t1) of `tiles`.
@@ -155,17 +160,17 @@ struct TreeSeg {
 struct TreeWalk {
   TreeSeq s;
   int b, u, t, c;
-  long long left;
+  int left;
   bool first;
-  __device__ TreeWalk(const TreeAttnArgs& a, int c_, int b0, long long off, long long count) {
+  __device__ TreeWalk(const TreeAttnArgs& a, int c_, int b0, int off, int count) {
     b = b0;
     c = c_;
     left = count;
     first = true;
     if (left > 0) {
       s = TreeSeq(a, b);
-      u = (int)(off / s.tiles);
-      t = (int)(off - (long long)u * s.tiles);
+      u = off / s.tiles;
+      t = off - u * s.tiles;
     }
   }
   __device__ bool next(const TreeAttnArgs& a, TreeSeg& g) {
@@ -174,7 +179,7 @@ struct TreeWalk {
       s = TreeSeq(a, ++b);
       u = 0;
     }
-    const int cnt = (int)min(left, (long long)(s.tiles - t));
+    const int cnt = min(left, s.tiles - t);
     g.b = b;
     g.kvh = u / s.groups;
     g.rg = u - g.kvh * s.groups;
@@ -198,19 +203,15 @@ struct TreeWalk {
 
 // ---- TMEM helpers of this kernel -----------------------------------------------------------
 
-// 128 consecutive columns of 32 lanes into registers (thread t of the warp reads lane base + t): four loads of 32
-// columns in flight, one wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
-  uint32_t r[128];
+// 64 consecutive columns of 32 lanes into registers (thread t of the warp reads lane base + t): two loads
+// in flight, one wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
+  uint32_t r[64];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
-      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
-      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
         "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
@@ -222,22 +223,11 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
         "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
         "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
         "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
-        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]),
-        "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]),
-        "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]),
-        "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]),
-        "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]),
-        "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]),
-        "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]),
-        "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
-        "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]),
-        "=r"(r[126]), "=r"(r[127])
-      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr), "r"(taddr + 32)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 registers into 32 consecutive columns, without waiting (tmem_wait_st follows).
@@ -263,28 +253,57 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// Registers of the calling warpgroup (all of its warps call it).
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
+__device__ __forceinline__ float max3(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
+
+// Ring positions of a segment's tiles: `ahead` tiles of K, then V and K in turn.
+__device__ __forceinline__ uint32_t tree_pos_k(int k, int ahead) { return k + max(0, k - ahead + 1); }
+__device__ __forceinline__ uint32_t tree_pos_v(int k, int ahead, int nt) { return k + min(nt, k + ahead); }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values along k in each 32-bit column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// MMAs whose shared-memory descriptors are given by their low word (address >> 4 in bits 0-13, leading
+// byte offset lbo above): the high word (stride 1024 bytes, version 1, 128-byte swizzle) is the same for all.
+constexpr uint32_t kTreeDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t lbo, uint32_t idesc,
+                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo | (lbo >> 4) << 16), "r"(b_lo | (lbo >> 4) << 16), "r"(idesc), "r"(accumulate), "r"(kTreeDescHi)
       : "memory");
 }
+
+// D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values along k in each 32-bit column.
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t lbo, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo | (lbo >> 4) << 16), "r"(idesc), "r"(accumulate), "r"(kTreeDescHi)
+      : "memory");
+}
+
+// A warp's common value, told to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// A position in the ring: stage, and the parity of its current lap.
+template <int STAGES>
+struct TreeRing {
+  uint32_t s = 0, phase = 0, laps = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1u;
+      laps = 1;
+    }
+  }
+};
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t tree_pack(float x, float y) {
@@ -338,7 +357,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   TreeMisc& ms = *reinterpret_cast<TreeMisc*>(smem + S::kMisc);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kHalves = D / 64;
-  constexpr int kHalf = kTreeKeys * 128;  // bytes of 64 columns of a tile
+  constexpr int kHalf = kTreeKeys * 128, kQHalf = 128 * 128;  // bytes of 64 columns of a K/V tile, of a q tile
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -347,11 +366,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&ms.s_full[s], 1);
       mbar_init(&ms.p_full[s], 4);
-      mbar_init(&ms.o_done[s], 1);
     }
+    mbar_init(&ms.o_done[0], 1);
+    mbar_init(&ms.o_done[1], 1);
     mbar_init(&ms.done, 1);
     ms.bad_any = 0;
     for (int i = 0; i < 8; ++i) ms.bad[i] = 0u;
@@ -363,118 +383,161 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
   griddep_wait();  // lengths, masks, q and K/V come from earlier kernels
   griddep_launch();
-  long long total, w0, w1;
-  int ctas;
   tc_fence_before();
-  tree_start<kTreeThreads>(a, ms.start, blockIdx.x, gridDim.x, blockIdx.x == 0, total, ctas, w0, w1);
+  const TreeCut cut = tree_start(a, ms.start, blockIdx.x, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  TreeWalk walk(a, blockIdx.x, ms.start.b, ms.start.off, w1 - w0);
+  TreeWalk walk(a, blockIdx.x, ms.start.b, ms.start.off, cut.at(blockIdx.x + 1) - cut.at(blockIdx.x));
   TreeSeg g;
 
-  if (warp >= 8) {
-    regs_dec<kTreeRegsOther>();
-    if (warp == kTreeLoadWarp) {
-      // ---- loads: Q of a segment, then K and V of its tiles, through one ring ----
-      if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-        uint32_t it = 0, seg = 0;
-        bool ok = true;
-        while (ok && walk.next(a, g)) {
-          const int z = g.b * a.Hkv + g.kvh;
-          const int qtiles = g.two ? 2 : 1;
-          if (seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&ms.q_full, qtiles * S::kTile);
-          const int qrow = z * a.N * a.G + g.rg * kTreeRows;
-          for (int h = 0; h < qtiles; ++h)
-            for (int e = 0; e < kHalves; ++e)
-              tma_load_2d(sQ + h * S::kTile + e * kHalf, &tmQ, &ms.q_full, e * 64, qrow + h * 128);
-          ++seg;
-          const int ct = (g.n + kTreeKeys - 1) / kTreeKeys;
-          for (int t = g.t0; ok && t < g.t1; ++t) {
-            const bool blk = t >= ct;
-            const int y = (blk ? t - ct : t) * kTreeKeys;
-            for (int kv = 0; kv < 2; ++kv, ++it) {
-              const uint32_t s = it % S::kStages, use = it / S::kStages;
-              if (use > 0 && !mbar_wait(&ms.empty[s], (use - 1) & 1, a.status)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive_expect_tx(&ms.full[s], S::kTile);
-              const CUtensorMap* m = kv == 0 ? (blk ? &tmKb : &tmK) : (blk ? &tmVb : &tmV);
-              for (int e = 0; e < kHalves; ++e) tma_load_3d(ring + s * S::kTile + e * kHalf, m, &ms.full[s], e * 64, y, z);
-            }
-          }
-        }
-        // copies in flight land before the CTA ends
-        if (seg > 0) mbar_wait(&ms.q_full, (seg - 1) & 1, a.status);
-        for (uint32_t k = it > (uint32_t)S::kStages ? it - S::kStages : 0; k < it; ++k)
-          mbar_wait(&ms.full[k % S::kStages], (k / S::kStages) & 1, a.status);
-      }
-    } else if (warp == kTreeMmaWarp) {
-      // ---- products: S = Q K^T, O += P V; stream j & 1 takes job j. The whole warp runs the loop, one
-      // elected thread issues: descriptors stay in uniform registers ----
-      constexpr uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
-      constexpr uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
-      const bool issue = elect_one();
-      const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc = sw128_desc(smem_u32(ring), 16, 1024), v_desc = sw128_desc(smem_u32(ring), kHalf, 1024);
-      uint32_t base = 0, seg = 0, cnt[2] = {0, 0};  // ring position of the segment; jobs of each stream
+  if (warp == kTreeLoadWarp) {
+    // ---- loads: Q of a segment, then K and V of its tiles in the order in which the MMA warp uses them ----
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      TreeRing<S::kStages> at;
+      uint32_t seg = 0;
       bool ok = true;
       while (ok && walk.next(a, g)) {
-        const int nt = g.t1 - g.t0;
-        const int jobs = g.two ? 2 * nt : nt;
-        ok = mbar_wait(&ms.q_full, seg & 1, a.status);
-        auto scores = [&](int j) {
-          const int k = g.two ? j >> 1 : j, st = j & 1;
-          const uint32_t pos = base + 2 * k, s = pos % S::kStages;
-          if (!(g.two && st) && !mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status)) return false;
-          tc_fence_after();
-          const uint64_t qd = q_desc + (g.two ? st * (S::kTile >> 4) : 0), kd = k_desc + s * (S::kTile >> 4);
-          const uint32_t to = tmem + st * 128;
-          if (issue) {
+        const int z = g.b * a.Hkv + g.kvh;
+        const int qtiles = g.two ? 2 : 1, ahead = min(g.two ? 2 : 4, g.t1 - g.t0);
+        if (seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&ms.q_full, qtiles * S::kQTile);
+        const int qrow = z * a.N * a.G + g.rg * kTreeRows;
+        for (int h = 0; h < qtiles; ++h)
+          for (int e = 0; e < kHalves; ++e)
+            tma_load_2d(sQ + h * S::kQTile + e * kQHalf, &tmQ, &ms.q_full, e * 64, qrow + h * 128);
+        ++seg;
+        const int ct = (g.n + kTreeKeys - 1) / kTreeKeys;
+        auto load = [&](int t, const CUtensorMap* cache, const CUtensorMap* tree) {
+          if (!mbar_wait(&ms.empty[at.s], at.phase ^ 1u, a.status)) return false;
+          mbar_arrive_expect_tx(&ms.full[at.s], S::kTile);
+          const bool blk = t >= ct;
+          const CUtensorMap* m = blk ? tree : cache;
+          const int y = (blk ? t - ct : t) * kTreeKeys;
+          uint8_t* dst = ring + at.s * S::kTile;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-              mma_ss(to, qd + off, kd + off, idS, i > 0 ? 1u : 0u);
-            }
-            mma_commit(&ms.s_full[st]);
-            if (!g.two || st) mma_commit(&ms.empty[s]);
-            if (j == jobs - 1) mma_commit(&ms.q_empty);
-          }
+          for (int e = 0; e < kHalves; ++e) tma_load_3d(dst + e * kHalf, m, &ms.full[at.s], e * 64, y, z);
+          at.step();
           return true;
         };
-        for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
-        for (int j = 0; ok && j < jobs; ++j) {
-          const int k = g.two ? j >> 1 : j, st = j & 1;
-          const uint32_t pos = base + 2 * k + 1, s = pos % S::kStages;
-          ok = mbar_wait(&ms.p_full[st], cnt[st] & 1, a.status);
-          if (ok && !(g.two && st)) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t vd = v_desc + s * (S::kTile >> 4);
-          const uint32_t to = tmem + 256 + st * 128, from = tmem + st * 128;
-          const uint32_t add = (g.two ? k == 0 : j < 2) ? 0u : 1u;  // the stream's first job starts its sums
-          if (issue) {
-#pragma unroll
-            for (int i = 0; i < kTreeKeys / 16; ++i) mma_ts(to, from + i * 8, vd + i * (2048 >> 4), idO, i > 0 ? 1u : add);
-            mma_commit(&ms.o_done[st]);
-            if (!g.two || st) mma_commit(&ms.empty[s]);
-          }
-          ++cnt[st];
-          if (j + 2 < jobs) ok = scores(j + 2);
+        for (int t = g.t0; ok && t < g.t0 + ahead; ++t) ok = load(t, &tmK, &tmKb);
+        for (int t = g.t0; ok && t < g.t1; ++t) {
+          ok = load(t, &tmV, &tmVb);
+          if (ok && t + ahead < g.t1) ok = load(t + ahead, &tmK, &tmKb);
         }
-        base += 2 * nt;
-        ++seg;
       }
-      if (issue) mma_commit(&ms.done);
-      mbar_wait(&ms.done, 0, a.status);
+      // copies in flight land before the CTA ends: the last use of each stage
+      if (seg > 0) mbar_wait(&ms.q_full, (seg - 1) & 1, a.status);
+      for (int k = 0; k < S::kStages; ++k) {
+        if (at.laps > 0 || k < (int)at.s) mbar_wait(&ms.full[k], k < (int)at.s ? at.phase : at.phase ^ 1u, a.status);
+      }
     }
-  } else {
-    regs_inc<kTreeRegs>();
+  } else if (warp == kTreeMmaWarp) {
+    // ---- products: S = Q K^T, O += P V. Tiles go through the ring in the order of their use: `ahead` tiles of
+    // K, then V and K in turn. A stream's jobs alternate between its two S buffers. The whole warp runs the
+    // loop on warp-uniform values (one warp's instruction latency is what this loop has to keep below the
+    // products' time), one elected thread issues ----
+    constexpr uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
+    constexpr uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
+    const bool issue = elect_one();
+    const uint32_t q_desc = uniform(smem_u32(sQ) >> 4), r_desc = uniform(smem_u32(ring) >> 4);
+    const uint32_t tm = uniform(tmem);
+    TreeRing<S::kStages> at;
+    uint32_t seg = 0, cs = 0, cp = 0;  // cs, cp: bit st = buffer of stream st's next score and sum job, bits 2-5 phases of p_full
+    bool ok = true;
+    auto scores = [&](uint32_t st, uint32_t qd, uint32_t kd) {
+      const uint32_t buf = 2 * st + ((cs >> st) & 1u);
+      cs ^= 1u << st;
+      const uint32_t to = tm + buf * 64;
+      if (issue) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          mma_ss_lo(to, qd + (((i >> 2) * kQHalf + (i & 3) * 32) >> 4), kd + (((i >> 2) * kHalf + (i & 3) * 32) >> 4), 16,
+                    idS, i > 0 ? 1u : 0u);
+        mma_commit(&ms.s_full[buf]);
+      }
+    };
+    auto sums = [&](uint32_t st, uint32_t vd, uint32_t add) {
+      const uint32_t buf = 2 * st + ((cp >> st) & 1u);
+      if (!mbar_wait(&ms.p_full[buf], (cp >> (2 + buf)) & 1u, a.status)) return false;
+      cp ^= (1u << st) | (4u << buf);
+      tc_fence_after();
+      const uint32_t to = tm + 256 + st * 128, from = tm + buf * 64;
+      if (issue) {
+#pragma unroll
+        for (int i = 0; i < kTreeKeys / 16; ++i) mma_ts_lo(to, from + i * 8, vd + i * (2048 >> 4), kHalf, idO, i > 0 ? 1u : add);
+        mma_commit(&ms.o_done[st]);
+      }
+      return true;
+    };
+    while (ok && walk.next(a, g)) {
+      const int nt = uniform(g.t1 - g.t0);
+      const bool two = uniform(g.two);
+      const int ahead = min(two ? 2 : 4, nt);
+      ok = mbar_wait(&ms.q_full, seg & 1, a.status);
+      for (int k = 0; ok && k < ahead; ++k) {
+        ok = mbar_wait(&ms.full[at.s], at.phase, a.status);
+        tc_fence_after();
+        const uint32_t kd = r_desc + at.s * (S::kTile >> 4);
+        if (two) {
+          scores(0, q_desc, kd);
+          scores(1, q_desc + (S::kQTile >> 4), kd);
+        } else {
+          scores(k & 1, q_desc, kd);
+        }
+        if (issue) {
+          mma_commit(&ms.empty[at.s]);
+          if (k == nt - 1) mma_commit(&ms.q_empty);
+        }
+        at.step();
+      }
+      for (int k = 0; ok && k < nt; ++k) {
+        const uint32_t vs = at.s, vp = at.phase;
+        at.step();
+        const uint32_t ks = at.s, kp = at.phase;
+        const bool more = k + ahead < nt;
+        const uint32_t vd = r_desc + vs * (S::kTile >> 4), kd = r_desc + ks * (S::kTile >> 4);
+        const uint32_t st = two ? 0 : k & 1;
+        ok = mbar_wait(&ms.full[vs], vp, a.status) && sums(st, vd, k > (two ? 0 : 1) ? 1u : 0u);
+        if (ok && !two && issue) mma_commit(&ms.empty[vs]);
+        if (ok && more) {
+          ok = mbar_wait(&ms.full[ks], kp, a.status);
+          tc_fence_after();
+          scores(st, q_desc, kd);
+        }
+        if (ok && two) {
+          ok = sums(1, vd, k > 0 ? 1u : 0u);
+          if (issue) mma_commit(&ms.empty[vs]);
+          if (more) scores(1, q_desc + (S::kQTile >> 4), kd);
+        }
+        if (more) {
+          if (issue) {
+            mma_commit(&ms.empty[ks]);
+            if (k + ahead == nt - 1) mma_commit(&ms.q_empty);
+          }
+          at.step();
+        }
+      }
+      ++seg;
+    }
+    if (issue) mma_commit(&ms.done);
+    mbar_wait(&ms.done, 0, a.status);
+  } else if (warp == kTreeNoteWarp) {
+    // ---- for the joining kernel: whether this range is the second of a unit that is cut ----
+    if (lane == 0) {
+      int4 note = make_int4(-1, 0, 0, 0);
+      const int c = blockIdx.x, t = walk.t, w0 = cut.at(c);
+      if (walk.next(a, g) && t > 0 && cut.at(c - 1) <= w0 - t) {
+        int last = c;
+        while (last + 1 < cut.ctas && cut.at(last + 1) < w0 - t + g.tiles) ++last;
+        note = make_int4(g.b, g.kvh, g.rg, last);
+      }
+      a.note[c] = note;
+    }
+  } else if (warp < 8) {
     // ---- softmax: stream 0 or 1, thread = row ----
     const int st = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -495,35 +558,64 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int k = g.two ? 0 : st; k < nt; k += g.two ? 1 : 2) {
         const int t = g.t0 + k, bt = t - ct;
         const bool blk = t >= ct;
-        const int lim = blk ? g.live - bt * kTreeKeys : g.n - t * kTreeKeys;  // keys of the tile, if below 128
-        if (ok) ok = mbar_wait(&ms.s_full[st], cnt & 1, a.status);
+        const int lim = blk ? g.live - bt * kTreeKeys : g.n - t * kTreeKeys;  // keys of the tile, if below 64
+        const uint32_t buf = cnt & 1;
+        unsigned long long see = ~0ull;
+        if (blk || lim < kTreeKeys) {
+          if (lim < kTreeKeys) see = (1ull << lim) - 1ull;
+          if (blk) see &= words[bt];
+          if (!(g.two && st)) {
+            // thread r < 64 looks after key r: V rows that nobody may see become zero, and values that
+            // are not finite leave the product
+            const uint32_t pos = base + tree_pos_v(k, g.two ? 2 : 4, nt), s = pos % S::kStages;
+            if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && r < kTreeKeys) {
+              uint8_t* vr = ring + s * S::kTile + r * 128;
+              bool bad = false;
+#pragma unroll 1
+              for (int q = 0; q < 8 * kHalves; ++q) {
+                uint4* p = reinterpret_cast<uint4*>(vr + (q >> 3) * kHalf + (q & 7) * 16);
+                if (r >= lim) {
+                  *p = make_uint4(0u, 0u, 0u, 0u);
+                } else if (blk) {
+                  const uint4 x = *p;
+                  if (!(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
+                        tree_finite<BF16>(x.w))) {
+                    bad = true;
+                    uint16_t* half = reinterpret_cast<uint16_t*>(p);
+                    for (int i = 0; i < 8; ++i)
+                      if (!tree_finite<BF16>(half[i])) half[i] = 0;
+                  }
+                }
+              }
+              if (bad) {
+                const int j = bt * kTreeKeys + r;
+                atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
+                ms.bad_any = 1;
+              }
+              fence_proxy_async_smem();
+            }
+          }
+        }
+        if (ok) ok = mbar_wait(&ms.s_full[2 * st + buf], (cnt >> 1) & 1, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && warp_ok) {
           tc_fence_after();
-          float v[128];
-          tmem_ld128(tS, v);
+          float v[64];
+          tmem_ld64(tS + buf * 64, v);
           if (blk || lim < kTreeKeys) {
-            uint32_t see[4];
+            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int left = lim - 32 * q;
-              see[q] = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
-            }
-            if (blk) {
-              const unsigned long long x = words[2 * bt], y = 2 * bt + 1 < a.words ? words[2 * bt + 1] : 0ull;
-              see[0] &= (uint32_t)x;
-              see[1] &= (uint32_t)(x >> 32);
-              see[2] &= (uint32_t)y;
-              see[3] &= (uint32_t)(y >> 32);
-            }
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (!(see[i >> 5] >> (i & 31) & 1u)) v[i] = -INFINITY;
+            for (int i = 0; i < 64; ++i)
+              if (!((i < 32 ? s0 >> i : s1 >> (i - 32)) & 1u)) v[i] = -INFINITY;
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-          for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+          for (int i = 4; i < 60; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], v[i + 2 * q], v[i + 2 * q + 1]);
+          const float mt = fmaxf(max3(mx[0], mx[1], fmaxf(v[60], v[61])), max3(mx[2], mx[3], fmaxf(v[62], v[63]))) * sl;
           if (first) {
             m = mt;
           } else {
@@ -549,60 +641,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           const float shift = m == -INFINITY ? 0.f : m - kTreeShift;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float p0 = fast_exp2(fmaf(v[h * 64 + 2 * i], sl, -shift));
-              const float p1 = fast_exp2(fmaf(v[h * 64 + 2 * i + 1], sl, -shift));
-              sum[(2 * i) & 3] += p0;
-              sum[(2 * i + 1) & 3] += p1;
-              pk[i] = tree_pack<BF16>(p0, p1);
-            }
-            tmem_put32(tS + h * 32, pk);
+          for (int i = 0; i < 32; ++i) {
+            const float p0 = fast_exp2(fmaf(v[2 * i], sl, -shift));
+            const float p1 = fast_exp2(fmaf(v[2 * i + 1], sl, -shift));
+            sum[(2 * i) & 3] += p0;
+            sum[(2 * i + 1) & 3] += p1;
+            pk[i] = tree_pack<BF16>(p0, p1);
           }
+          tmem_put32(tS + buf * 64, pk);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
-        if ((blk || lim < kTreeKeys) && !(g.two && st)) {
-          // thread r looks after key r: V rows that nobody may see become zero, and values that are
-          // not finite leave the product
-          const uint32_t pos = base + 2 * k + 1, s = pos % S::kStages;
-          if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            uint8_t* vr = ring + s * S::kTile + r * 128;
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < kHalves; ++e)
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                uint4* p = reinterpret_cast<uint4*>(vr + e * kHalf + q * 16);
-                if (r >= lim) {
-                  *p = make_uint4(0u, 0u, 0u, 0u);
-                } else if (blk) {
-                  const uint4 x = *p;
-                  if (!(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
-                        tree_finite<BF16>(x.w))) {
-                    bad = true;
-                    uint16_t* half = reinterpret_cast<uint16_t*>(p);
-                    for (int i = 0; i < 8; ++i)
-                      if (!tree_finite<BF16>(half[i])) half[i] = 0;
-                  }
-                }
-              }
-            if (bad) {
-              const int j = bt * kTreeKeys + r;
-              atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
-              ms.bad_any = 1;
-            }
-            fence_proxy_async_smem();
-          }
-        }
         tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&ms.p_full[st]);
+        if (ok && lane == 0) mbar_arrive(&ms.p_full[2 * st + buf]);
         first = false;
         ++cnt;
       }
@@ -610,6 +664,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
       // ---- the segment's sums ----
       const bool mine = g.two || nt > st;  // this stream had a job
+      // the last two products may both be under way: one phase after the other
+      if (ok && mine && cnt > 1) ok = mbar_wait(&ms.o_done[st], (cnt - 2) & 1, a.status);
       if (ok && mine) ok = mbar_wait(&ms.o_done[st], (cnt - 1) & 1, a.status);
       ok = __all_sync(0xffffffffu, ok);
       float w_own = 1.f, w_other = 0.f;
@@ -699,52 +755,67 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // ---- joining the parts of a cut unit ---------------------------------------------------------
 
-// CTA x looks at the start of range x: where that cuts a unit, and is the first cut of it, the
-// CTA joins 32 rows x 32 columns of the unit, thread = (row, 4 columns). Parts are added in
-// key order: out = sum_c w_c O_c / sum_c w_c l_c, w_c = 2^(m_c - max m).
+// CTA x reads note x + 1: where that range is the second of a cut unit, it joins 32 rows x 32
+// columns of the unit's parts, thread = (row, 4 columns), in key order:
+//     out = sum_c w_c O_c / sum_c w_c l_c,   w_c = 2^(m_c - max m).
+// The parts' weights are computed once for a row, by the 8 threads that share it.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 64;  // parts whose weights are held at a time
 
-__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a, int sms) {
-  __shared__ TreeStart start;
+__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a) {
+  __shared__ float w[kJoinParts][32];
+  __shared__ float red[8][32];
   griddep_wait();
   griddep_launch();
-  const int c = blockIdx.x + 1;
-  long long total, w0, w1;
-  int ctas;
-  tree_start<kJoinThreads>(a, start, c, sms, false, total, ctas, w0, w1);
-  const int b = start.b;
-  if (b < 0) return;
-  const TreeSeq s(a, b);
-  const int u = (int)(start.off / s.tiles), t = (int)(start.off - (long long)u * s.tiles);
-  const long long g0 = w0 - t, g1 = g0 + s.tiles;
-  if (t == 0 || tree_cut(total, ctas, c - 1) > g0) return;  // no cut, or not the unit's first
-  const int kvh = u / s.groups, rg = u - kvh * s.groups;
-  const int c0 = c - 1;
-  int c1 = c;
-  while (c1 + 1 < ctas && tree_cut(total, ctas, c1 + 1) < g1) ++c1;
-  const int lrow = blockIdx.y * 32 + (threadIdx.x & 31);
-  if (rg * kTreeRows + lrow >= s.live * a.G) return;
-  const int e4 = blockIdx.z * 8 + (threadIdx.x >> 5);
+  const int4 note = __ldcg(&a.note[blockIdx.x + 1]);
+  if (note.x < 0) return;
+  const int r = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int live = a.n_nodes ? min(max(a.n_nodes[note.x], 0), a.N) : a.N;
+  const int lrow = blockIdx.y * 32 + r, rows = live * a.G - note.z * kTreeRows;
+  if ((int)blockIdx.y * 32 >= rows) return;
+  const int c0 = blockIdx.x, n = note.w - c0 + 1;
   // slot of part i: a range that starts inside the unit uses its CTA's first slot
-  auto slot = [&](int i) { return (size_t)(2 * i + (i == c0 ? 1 : 0)); };
+  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
+  const float2* ml = a.part_ml + lrow;
   float top = -INFINITY;
-  for (int i = c0; i <= c1; ++i) top = fmaxf(top, __ldcg(&a.part_ml[slot(i) * kTreeRows + lrow]).x);
+#pragma unroll 4
+  for (int i = part; i < n; i += 8) top = fmaxf(top, __ldcg(ml + slot(i) * kTreeRows).x);
+  red[part][r] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i][r]);
   const float ref = top == -INFINITY ? 0.f : top;
+  const int e4 = blockIdx.z * 8 + part;
+  const float4* po = a.part_o + (size_t)e4 * kTreeRows + lrow;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = c0; i <= c1; ++i) {
-    const float2 ml = __ldcg(&a.part_ml[slot(i) * kTreeRows + lrow]);
-    const float4 x = __ldcg(&a.part_o[(slot(i) * (a.d / 4) + e4) * kTreeRows + lrow]);
-    const float w = exp2f(ml.x - ref);
-    l += ml.y * w;
-    o.x += x.x * w;
-    o.y += x.y * w;
-    o.z += x.z * w;
-    o.w += x.w * w;
+  for (int i0 = 0; i0 < n; i0 += kJoinParts) {
+    const int cnt = min(kJoinParts, n - i0);
+    __syncthreads();
+    for (int i = part; i < cnt; i += 8) {
+      const float2 x = __ldcg(ml + slot(i0 + i) * kTreeRows);
+      w[i][r] = exp2f(x.x - ref);
+      l += x.y * w[i][r];
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = 0; i < cnt; ++i) {
+      const float4 x = __ldcg(po + slot(i0 + i) * (a.d / 4) * kTreeRows);
+      const float f = w[i][r];
+      o.x += x.x * f;
+      o.y += x.y * f;
+      o.z += x.z * f;
+      o.w += x.w * f;
+    }
   }
+  red[part][r] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) l += red[i][r];
+  if (lrow >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const size_t to = tree_out_at(a, b, kvh, rg * kTreeRows + lrow) + e4 * 4;
+  const size_t to = tree_out_at(a, note.x, note.y, note.z * kTreeRows + lrow) + e4 * 4;
   const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   if (a.out_type == ORTHRUS_FP16) {
     *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(tree_pack<false>(y[0], y[1]), tree_pack<false>(y[2], y[3]));
