@@ -43,10 +43,10 @@ orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* wo
   a.part_o = (float4*)workspace;
   a.part_ml = (float2*)(a.part_o + (size_t)2 * num_sms() * kTreeRows * (a.d / 4));
   a.note = (int4*)(a.part_ml + (size_t)2 * num_sms() * kTreeRows);
-  // the line of tiles is counted in 31 bits
+  // the costs of all tiles are counted in 31 bits
   const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
   const long long units = (long long)a.B * a.Hkv * (((long long)a.N * a.G + kTreeRows - 1) / kTreeRows);
-  if (units * tiles > INT32_MAX) return ORTHRUS_ERR_UNSUPPORTED;
+  if (units * tiles > INT32_MAX / kTreeCost2) return ORTHRUS_ERR_UNSUPPORTED;
   const CUtensorMapDataType dt = a.bf16 ? kBF16 : kF16;
   const uint64_t z = (uint64_t)a.B * a.Hkv;
   CUtensorMap m[5];

@@ -44,12 +44,12 @@
 
 namespace orthrus {
 
-constexpr int kTreeThreads = 384;  // 8 softmax warps, load, MMA and note warp, one idle
+constexpr int kTreeThreads = 384;  // 8 softmax warps, a load warp, two MMA warps, a note warp
 constexpr int kTreeKeys = 64;      // keys of a tile: one visibility word
 constexpr int kTreeRows = 256;      // rows of a unit
 constexpr float kTreeSlack = 8.f;   // how far scores may exceed the reference (log2)
 constexpr float kTreeShift = 7.f;   // factor on the weights (log2)
-constexpr int kTreeLoadWarp = 8, kTreeMmaWarp = 9, kTreeNoteWarp = 10;
+constexpr int kTreeLoadWarp = 8, kTreeMmaWarp = 9, kTreeNoteWarp = 11;  // MMA warps 9 and 10
 
 template <int D>
 struct TreeSmem {
@@ -62,12 +62,12 @@ struct TreeSmem {
   static constexpr int kBytes = 1024 + kMisc + 2048;  // 1024: alignment of the dynamic part
 };
 
-struct TreeStart {  // where a CTA's range of tiles starts
+struct TreeStart {  // where a CTA's work starts
   int scan[kTreeThreads / 32], b, off;
 };
 
 struct TreeMisc {
-  uint64_t full[20], empty[20], q_full, q_empty, s_full[4], p_full[4], o_done[2], done;  // s_full, p_full: 2 stream + buffer
+  uint64_t full[20], empty[20], q_full, q_empty, s_full[4], p_full[4], o_done[2], done[2], seg_done;  // s_full, p_full: 2 stream + buffer
   uint32_t tmem;
   int bad_any;
   unsigned int bad[8];  // tree rows with values that are not finite (this segment)
@@ -76,77 +76,130 @@ struct TreeMisc {
 };
 static_assert(sizeof(TreeMisc) <= 2048, "misc area");
 
-// ---- the line of tiles --------------------------------------------------------------------
+// ---- who works on what ------------------------------------------------------------------
+
+constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile's relative time with up to 128 rows, with more
+constexpr int kTreeSwitch = 16;                // and that of a second segment in a CTA
+constexpr int kTreeMinTiles = 4;               // tiles of a part at least, in the even division
 
 struct TreeSeq {
-  int n, live, tiles, groups;  // clamped length, nodes, tiles of a unit, row groups
+  int n, live, tiles, groups, big;  // clamped length, nodes, tiles of a unit, row groups, groups of more than 128 rows
   __device__ TreeSeq() {}
   __device__ TreeSeq(const TreeAttnArgs& a, int b) {
     n = min(max(a.len[b], 0), a.cap);
     live = a.n_nodes ? min(max(a.n_nodes[b], 0), a.N) : a.N;
-    groups = (live * a.G + kTreeRows - 1) / kTreeRows;
+    const int rows = live * a.G;
+    groups = (rows + kTreeRows - 1) / kTreeRows;
+    big = (rows + kTreeRows - 129) / kTreeRows;
     tiles = (n + kTreeKeys - 1) / kTreeKeys + (live + kTreeKeys - 1) / kTreeKeys;
   }
-  __device__ int work(int Hkv) const { return groups * Hkv * tiles; }
+  __device__ int cost(int rg) const { return rg < big ? kTreeCost2 : kTreeCost1; }  // of a tile
+  __device__ int head() const { return tiles * (big * kTreeCost2 + (groups - big) * kTreeCost1); }  // of a KV head
 };
 
-// The line of `total` tiles in `ctas` ranges whose lengths differ by at most one: start of range c.
-// (Tiles of all units fit 31 bits, which the host checks with the capacity.)
-struct TreeCut {
-  int total, ctas, each, more;
-  __device__ TreeCut(int total_, int sms) {
-    total = total_;
-    ctas = max(1, min(sms, total));
-    each = total / ctas;
-    more = total - each * ctas;
-  }
+// The division of the work. Even: every unit is cut into parts of its own, about as many as its share of
+// the CTAs, and a CTA has one part. Line: the costs of all tiles form one line, cut into ranges of equal
+// length, and a CTA has the tiles that start in its range, of one or several units. The even division is
+// taken where its largest part does not exceed the range by more than a switch of units costs.
+// (All costs fit 31 bits, which the host checks with the capacity.)
+struct TreeShare {
+  int total, ctas, each, more;  // line
+  float per_cost;               // CTAs for a unit of cost: even
+  bool even;
   __device__ int at(int c) const { return min(total, c * each + min(c, more)); }
+  __device__ int parts(const TreeSeq& s, int rg) const {
+    const int n = (int)(s.tiles * s.cost(rg) * per_cost), most = (s.tiles + kTreeMinTiles - 1) / kTreeMinTiles;
+    return max(1, min(n, most));
+  }
+  __device__ int head_parts(const TreeSeq& s) const {
+    return (s.big ? s.big * parts(s, 0) : 0) + (s.groups > s.big ? parts(s, s.groups - 1) : 0);
+  }
+  __device__ int largest(const TreeSeq& s) const {  // cost of a sequence's largest part
+    int x = 0;
+    for (int rg = 0; rg < s.groups; rg += max(1, s.groups - 1)) {
+      const int n = parts(s, rg);
+      x = max(x, (s.tiles + n - 1) / n * s.cost(rg));
+    }
+    return x;
+  }
 };
 
-// Finds the start of range c of the line of tiles: sequence st.b and tile st.off among that
-// sequence's (st.b = -1 if the range is empty). Called by all threads of the CTA; the sums
-// before each sequence are an exclusive scan over the CTA, every thread holding a contiguous
-// share of the sequences.
-__device__ __forceinline__ TreeCut tree_start(const TreeAttnArgs& a, TreeStart& st, int c, int sms) {
-  const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
-  const int lo = min(a.B, (int)threadIdx.x * per), hi = min(a.B, lo + per);
-  int own = 0;
-  for (int b = lo; b < hi; ++b) {
-    own += TreeSeq(a, b).work(a.Hkv);
-    const int n = a.len[b];
-    if (c == 0 && (n < 0 || n > a.cap)) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
-  }
-  int inc = own;
+// Sum over the CTA's threads, and of those before this one.
+__device__ __forceinline__ int tree_scan(TreeStart& st, int own, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
   if (lane == 31) st.scan[warp] = inc;
-  if (threadIdx.x == 0) st.b = -1;
   __syncthreads();
-  int at = inc - own, total = 0;
+  int at = inc - own;
+  total = 0;
 #pragma unroll
   for (int w = 0; w < kTreeThreads / 32; ++w) {
     if (w < warp) at += st.scan[w];
     total += st.scan[w];
   }
-  const TreeCut cut(total, sms);
-  const int w0 = cut.at(c);
-  if (w0 < total && w0 >= at && w0 < at + own) {
+  return at;
+}
+
+// Finds the division, and where CTA c starts in it: sequence st.b (-1: nothing to do) and the cost
+// (line) or part (even) st.off among that sequence's. Called by all threads of the CTA, which
+// hold contiguous shares of the sequences.
+__device__ __forceinline__ TreeShare tree_start(const TreeAttnArgs& a, TreeStart& st, int c, int sms) {
+  const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
+  const int lo = min(a.B, (int)threadIdx.x * per), hi = min(a.B, lo + per);
+  int own = 0, units = 0;
+  for (int b = lo; b < hi; ++b) {
+    const TreeSeq s(a, b);
+    own += s.head() * a.Hkv;
+    units += s.groups * a.Hkv;
+    const int n = a.len[b];
+    if (c == 0 && (n < 0 || n > a.cap)) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
+  }
+  if (threadIdx.x == 0) st.b = -1;
+  TreeShare d;
+  int at = tree_scan(st, own, d.total);
+  d.ctas = max(1, min(sms, d.total / kTreeCost2));
+  d.each = d.total / d.ctas;
+  d.more = d.total - d.each * d.ctas;
+  d.per_cost = (float)sms / (float)max(1, d.total);
+  int parts = 0;
+  bool even = true;
+  for (int b = lo; b < hi; ++b) {
+    const TreeSeq s(a, b);
+    parts += d.head_parts(s) * a.Hkv;
+    even = even && d.largest(s) <= d.each + kTreeSwitch;
+  }
+  even = __syncthreads_and(even && units <= sms);
+  d.even = even;
+  if (even) {  // with at most as many parts as CTAs
+    int all;
+    const int before = tree_scan(st, parts, all);
+    d.even = all <= sms;
+    if (d.even) {
+      own = parts;
+      at = before;
+      d.ctas = all;
+    }
+  }
+  const int mine = d.even ? c : d.at(c);
+  if (c < d.ctas && mine >= at && mine < at + own) {
     for (int b = lo;; ++b) {
-      const int w = TreeSeq(a, b).work(a.Hkv);
-      if (w0 < at + w) {
+      const TreeSeq s(a, b);
+      const int w = (d.even ? d.head_parts(s) : s.head()) * a.Hkv;
+      if (mine < at + w) {
         st.b = b;
-        st.off = w0 - at;
+        st.off = mine - at;
         break;
       }
       at += w;
     }
   }
   __syncthreads();
-  return cut;
+  return d;
 }
 
 // The part of a unit that one CTA works on: tiles [t0, t1) of `tiles`.
@@ -159,43 +212,73 @@ struct TreeSeg {
 // A CTA's segments in order; every role walks them by itself.
 struct TreeWalk {
   TreeSeq s;
-  int b, u, t, c;
-  int left;
+  int b, kvh, rg, t, t1, c, left;  // left: the range's cost from the unit's start on (line)
+  int part, parts;                 // of the unit (even)
   bool first;
-  __device__ TreeWalk(const TreeAttnArgs& a, int c_, int b0, int off, int count) {
-    b = b0;
+  __device__ TreeWalk(const TreeAttnArgs& a, const TreeShare& d, const TreeStart& st, int c_) {
     c = c_;
-    left = count;
+    b = st.b;
     first = true;
-    if (left > 0) {
-      s = TreeSeq(a, b);
-      u = off / s.tiles;
-      t = off - u * s.tiles;
+    left = 0;
+    part = 0;
+    parts = d.even ? 1 : 0;
+    if (b < 0) return;
+    s = TreeSeq(a, b);
+    const int head = d.even ? d.head_parts(s) : s.head();
+    kvh = st.off / head;
+    int r = st.off - kvh * head;
+    const int n = d.even ? parts_of(d, 0) : s.tiles * s.cost(0);  // of a unit, all but the last
+    rg = min(r / n, s.groups - 1);
+    r -= rg * n;
+    if (d.even) {
+      part = r;
+      parts = parts_of(d, rg);
+      t = s.tiles * part / parts;
+      t1 = s.tiles * (part + 1) / parts;
+      left = 1;
+    } else {
+      const int w = s.cost(rg);
+      left = d.at(c + 1) - d.at(c) + r;
+      t = (r + w - 1) / w;
+      if (t == s.tiles) {
+        left -= s.tiles * w;
+        t = 0;
+        ++rg;
+      }
     }
   }
+  __device__ int parts_of(const TreeShare& d, int g) const { return d.parts(s, g); }
   __device__ bool next(const TreeAttnArgs& a, TreeSeg& g) {
     if (left <= 0) return false;
-    while (u >= s.groups * a.Hkv) {
-      s = TreeSeq(a, ++b);
-      u = 0;
+    if (parts == 0) {
+      if (rg >= s.groups) {
+        rg = 0;
+        ++kvh;
+      }
+      while (s.groups == 0 || kvh >= a.Hkv) {
+        s = TreeSeq(a, ++b);
+        kvh = 0;
+      }
+      const int w = s.cost(rg);
+      t1 = min(s.tiles, (left + w - 1) / w);
     }
-    const int cnt = min(left, s.tiles - t);
     g.b = b;
-    g.kvh = u / s.groups;
-    g.rg = u - g.kvh * s.groups;
+    g.kvh = kvh;
+    g.rg = rg;
     g.n = s.n;
     g.live = s.live;
     g.tiles = s.tiles;
     g.t0 = t;
-    g.t1 = t + cnt;
-    g.two = s.live * a.G - g.rg * kTreeRows > 128;
+    g.t1 = t1;
+    g.two = rg < s.big;
     g.slot = 2 * c + (first && t > 0 ? 0 : 1);
     first = false;
-    left -= cnt;
-    t += cnt;
-    if (t == s.tiles) {
+    if (parts == 0 && t1 == s.tiles) {
+      left -= s.tiles * s.cost(rg);
       t = 0;
-      ++u;
+      ++rg;
+    } else {
+      left = 0;
     }
     return true;
   }
@@ -362,17 +445,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&ms.full[s], 1);
-      mbar_init(&ms.empty[s], 1);
+      mbar_init(&ms.empty[s], 2);
     }
     mbar_init(&ms.q_full, 1);
-    mbar_init(&ms.q_empty, 1);
+    mbar_init(&ms.q_empty, 2);
     for (int s = 0; s < 4; ++s) {
       mbar_init(&ms.s_full[s], 1);
       mbar_init(&ms.p_full[s], 4);
     }
     mbar_init(&ms.o_done[0], 1);
     mbar_init(&ms.o_done[1], 1);
-    mbar_init(&ms.done, 1);
+    mbar_init(&ms.seg_done, 2);
+    mbar_init(&ms.done[0], 1);
+    mbar_init(&ms.done[1], 1);
     ms.bad_any = 0;
     for (int i = 0; i < 8; ++i) ms.bad[i] = 0u;
     fence_barrier_init();
@@ -384,10 +469,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   griddep_wait();  // lengths, masks, q and K/V come from earlier kernels
   griddep_launch();
   tc_fence_before();
-  const TreeCut cut = tree_start(a, ms.start, blockIdx.x, gridDim.x);
+  const TreeShare share = tree_start(a, ms.start, blockIdx.x, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  TreeWalk walk(a, blockIdx.x, ms.start.b, ms.start.off, cut.at(blockIdx.x + 1) - cut.at(blockIdx.x));
+  TreeWalk walk(a, share, ms.start, blockIdx.x);
   TreeSeg g;
 
   if (warp == kTreeLoadWarp) {
@@ -402,14 +487,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       while (ok && walk.next(a, g)) {
         const int z = g.b * a.Hkv + g.kvh;
         const int qtiles = g.two ? 2 : 1, ahead = min(g.two ? 2 : 4, g.t1 - g.t0);
-        if (seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&ms.q_full, qtiles * S::kQTile);
-        const int qrow = z * a.N * a.G + g.rg * kTreeRows;
-        for (int h = 0; h < qtiles; ++h)
-          for (int e = 0; e < kHalves; ++e)
-            tma_load_2d(sQ + h * S::kQTile + e * kQHalf, &tmQ, &ms.q_full, e * 64, qrow + h * 128);
-        ++seg;
         const int ct = (g.n + kTreeKeys - 1) / kTreeKeys;
         auto load = [&](int t, const CUtensorMap* cache, const CUtensorMap* tree) {
           if (!mbar_wait(&ms.empty[at.s], at.phase ^ 1u, a.status)) return false;
@@ -423,7 +500,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           at.step();
           return true;
         };
+        // the first K tiles fill free stages while the last segment's scores still read its q
         for (int t = g.t0; ok && t < g.t0 + ahead; ++t) ok = load(t, &tmK, &tmKb);
+        if (ok && seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&ms.q_full, qtiles * S::kQTile);
+        const int qrow = z * a.N * a.G + g.rg * kTreeRows;
+        for (int h = 0; h < qtiles; ++h)
+          for (int e = 0; e < kHalves; ++e)
+            tma_load_2d(sQ + h * S::kQTile + e * kQHalf, &tmQ, &ms.q_full, e * 64, qrow + h * 128);
+        ++seg;
         for (int t = g.t0; ok && t < g.t1; ++t) {
           ok = load(t, &tmV, &tmVb);
           if (ok && t + ahead < g.t1) ok = load(t + ahead, &tmK, &tmKb);
@@ -435,105 +521,104 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (at.laps > 0 || k < (int)at.s) mbar_wait(&ms.full[k], k < (int)at.s ? at.phase : at.phase ^ 1u, a.status);
       }
     }
-  } else if (warp == kTreeMmaWarp) {
-    // ---- products: S = Q K^T, O += P V. Tiles go through the ring in the order of their use: `ahead` tiles of
-    // K, then V and K in turn. A stream's jobs alternate between its two S buffers. The whole warp runs the
-    // loop on warp-uniform values (one warp's instruction latency is what this loop has to keep below the
-    // products' time), one elected thread issues ----
+  } else if (warp == kTreeMmaWarp || warp == kTreeMmaWarp + 1) {
+    // ---- products: S = Q K^T, two jobs of a stream ahead of O += P V. With more than 128 rows the streams
+    // have a warp each (the instruction latency of this loop, not the products, would otherwise set the
+    // pace) and a stage is free after a commit of each; else the first warp serves both streams, sees every
+    // stage in order, and commits twice. The whole warp runs the loop on warp-uniform values, one elected
+    // thread issues ----
     constexpr uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
     constexpr uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
     const bool issue = elect_one();
-    const uint32_t q_desc = uniform(smem_u32(sQ) >> 4), r_desc = uniform(smem_u32(ring) >> 4);
-    const uint32_t tm = uniform(tmem);
-    TreeRing<S::kStages> at;
-    uint32_t seg = 0, cs = 0, cp = 0;  // cs, cp: bit st = buffer of stream st's next score and sum job, bits 2-5 phases of p_full
-    bool ok = true;
-    auto scores = [&](uint32_t st, uint32_t qd, uint32_t kd) {
-      const uint32_t buf = 2 * st + ((cs >> st) & 1u);
-      cs ^= 1u << st;
-      const uint32_t to = tm + buf * 64;
-      if (issue) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          mma_ss_lo(to, qd + (((i >> 2) * kQHalf + (i & 3) * 32) >> 4), kd + (((i >> 2) * kHalf + (i & 3) * 32) >> 4), 16,
-                    idS, i > 0 ? 1u : 0u);
-        mma_commit(&ms.s_full[buf]);
-      }
-    };
-    auto sums = [&](uint32_t st, uint32_t vd, uint32_t add) {
-      const uint32_t buf = 2 * st + ((cp >> st) & 1u);
-      if (!mbar_wait(&ms.p_full[buf], (cp >> (2 + buf)) & 1u, a.status)) return false;
-      cp ^= (1u << st) | (4u << buf);
-      tc_fence_after();
-      const uint32_t to = tm + 256 + st * 128, from = tm + buf * 64;
-      if (issue) {
-#pragma unroll
-        for (int i = 0; i < kTreeKeys / 16; ++i) mma_ts_lo(to, from + i * 8, vd + i * (2048 >> 4), kHalf, idO, i > 0 ? 1u : add);
-        mma_commit(&ms.o_done[st]);
-      }
-      return true;
-    };
+    const uint32_t mine = warp - kTreeMmaWarp;
+    const uint32_t r_desc = uniform(smem_u32(ring) >> 4), q_desc = uniform(smem_u32(sQ) >> 4), tm = uniform(tmem);
+    uint32_t base = 0, seg = 0, c0 = 0, c1 = 0;  // ring position of the segment; segments, jobs of each stream so far
+    bool ok = true, was_two = false;
     while (ok && walk.next(a, g)) {
       const int nt = uniform(g.t1 - g.t0);
       const bool two = uniform(g.two);
-      const int ahead = min(two ? 2 : 4, nt);
-      ok = mbar_wait(&ms.q_full, seg & 1, a.status);
-      for (int k = 0; ok && k < ahead; ++k) {
-        ok = mbar_wait(&ms.full[at.s], at.phase, a.status);
-        tc_fence_after();
-        const uint32_t kd = r_desc + at.s * (S::kTile >> 4);
-        if (two) {
-          scores(0, q_desc, kd);
-          scores(1, q_desc + (S::kQTile >> 4), kd);
-        } else {
-          scores(k & 1, q_desc, kd);
-        }
-        if (issue) {
-          mma_commit(&ms.empty[at.s]);
-          if (k == nt - 1) mma_commit(&ms.q_empty);
-        }
-        at.step();
-      }
-      for (int k = 0; ok && k < nt; ++k) {
-        const uint32_t vs = at.s, vp = at.phase;
-        at.step();
-        const uint32_t ks = at.s, kp = at.phase;
-        const bool more = k + ahead < nt;
-        const uint32_t vd = r_desc + vs * (S::kTile >> 4), kd = r_desc + ks * (S::kTile >> 4);
-        const uint32_t st = two ? 0 : k & 1;
-        ok = mbar_wait(&ms.full[vs], vp, a.status) && sums(st, vd, k > (two ? 0 : 1) ? 1u : 0u);
-        if (ok && !two && issue) mma_commit(&ms.empty[vs]);
-        if (ok && more) {
-          ok = mbar_wait(&ms.full[ks], kp, a.status);
+      const int ahead = two ? 2 : 4;
+      // seg_done: both warps have issued a segment's products and they are complete. Each warp sees every
+      // phase: before its scores where the streams change hands (the S buffers' last readers were issued by
+      // the other warp), else before its sums
+      const bool early = two != was_two;
+      was_two = two;
+      if (early && seg > 0) ok = mbar_wait(&ms.seg_done, (seg - 1) & 1, a.status);
+      if (two || mine == 0) {
+        if (ok) ok = mbar_wait(&ms.q_full, seg & 1, a.status);
+        const uint32_t qd = q_desc + (two ? mine * (S::kQTile >> 4) : 0);
+        // job of tile k: its stream, and the stream's job number
+        auto stream = [&](int k) { return two ? mine : (uint32_t)k & 1u; };
+        auto job = [&](int k) { return two ? (mine ? c1 : c0) + k : ((k & 1) ? c1 : c0) + (k >> 1); };
+        auto scores = [&](int k) {
+          const uint32_t pos = base + tree_pos_k(k, ahead), s = pos % S::kStages, buf = 2 * stream(k) + (job(k) & 1u);
+          if (!mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status)) return false;
           tc_fence_after();
-          scores(st, q_desc, kd);
-        }
-        if (ok && two) {
-          ok = sums(1, vd, k > 0 ? 1u : 0u);
-          if (issue) mma_commit(&ms.empty[vs]);
-          if (more) scores(1, q_desc + (S::kQTile >> 4), kd);
-        }
-        if (more) {
+          const uint32_t to = tm + buf * 64, kd = r_desc + s * (S::kTile >> 4);
           if (issue) {
-            mma_commit(&ms.empty[ks]);
-            if (k + ahead == nt - 1) mma_commit(&ms.q_empty);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              mma_ss_lo(to, qd + (((i >> 2) * kQHalf + (i & 3) * 32) >> 4), kd + (((i >> 2) * kHalf + (i & 3) * 32) >> 4), 16,
+                        idS, i > 0 ? 1u : 0u);
+            mma_commit(&ms.s_full[buf]);
+            mma_commit(&ms.empty[s]);
+            if (!two) mma_commit(&ms.empty[s]);
+            if (k == nt - 1) {
+              mma_commit(&ms.q_empty);
+              if (!two) mma_commit(&ms.q_empty);
+            }
           }
-          at.step();
+          return true;
+        };
+        for (int k = 0; ok && k < ahead && k < nt; ++k) ok = scores(k);
+        if (ok && !early && seg > 0) ok = mbar_wait(&ms.seg_done, (seg - 1) & 1, a.status);
+        for (int k = 0; ok && k < nt; ++k) {
+          const uint32_t pos = base + tree_pos_v(k, ahead, nt), s = pos % S::kStages;
+          const uint32_t st = stream(k), n = job(k), buf = 2 * st + (n & 1u);
+          ok = mbar_wait(&ms.p_full[buf], (n >> 1) & 1u, a.status) &&
+               mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t to = tm + 256 + st * 128, from = tm + buf * 64, vd = r_desc + s * (S::kTile >> 4);
+          const uint32_t add = k >= (two ? 1 : 2) ? 1u : 0u;  // the stream's first job of the segment starts its sums
+          if (issue) {
+#pragma unroll
+            for (int i = 0; i < kTreeKeys / 16; ++i)
+              mma_ts_lo(to, from + i * 8, vd + i * (2048 >> 4), kHalf, idO, i > 0 ? 1u : add);
+            mma_commit(&ms.o_done[st]);
+            mma_commit(&ms.empty[s]);
+            if (!two) mma_commit(&ms.empty[s]);
+          }
+          if (k + ahead < nt) ok = scores(k + ahead);
         }
+        if (ok && issue) mma_commit(&ms.seg_done);
+      } else {
+        if (ok && !early && seg > 0) ok = mbar_wait(&ms.seg_done, (seg - 1) & 1, a.status);
+        if (ok && issue) mbar_arrive(&ms.seg_done);
       }
+      c0 += two ? nt : (nt + 1) >> 1;
+      c1 += two ? nt : nt >> 1;
+      base += 2 * nt;
       ++seg;
     }
-    if (issue) mma_commit(&ms.done);
-    mbar_wait(&ms.done, 0, a.status);
+    if (issue) mma_commit(&ms.done[mine]);
+    mbar_wait(&ms.done[mine], 0, a.status);
   } else if (warp == kTreeNoteWarp) {
-    // ---- for the joining kernel: whether this range is the second of a unit that is cut ----
+    // ---- for the joining kernel: whether this CTA has the second part of a unit that is cut ----
     if (lane == 0) {
       int4 note = make_int4(-1, 0, 0, 0);
-      const int c = blockIdx.x, t = walk.t, w0 = cut.at(c);
-      if (walk.next(a, g) && t > 0 && cut.at(c - 1) <= w0 - t) {
+      const int c = blockIdx.x, r = walk.left - (share.at(c + 1) - share.at(c));  // line: the unit's cost before the range
+      if (walk.next(a, g) && g.t0 > 0) {
         int last = c;
-        while (last + 1 < cut.ctas && cut.at(last + 1) < w0 - t + g.tiles) ++last;
-        note = make_int4(g.b, g.kvh, g.rg, last);
+        if (share.even) {
+          last = walk.part == 1 ? c + walk.parts - 2 : -1;
+        } else {
+          const int u0 = share.at(c) - r, tail = u0 + (g.tiles - 1) * (g.two ? kTreeCost2 : kTreeCost1);
+          if (share.at(c - 1) > u0) last = -1;
+          else
+            while (last + 1 < share.ctas && share.at(last + 1) <= tail) ++last;
+        }
+        if (last >= 0) note = make_int4(g.b, g.kvh, g.rg, last);
       }
       a.note[c] = note;
     }
@@ -564,42 +649,46 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (blk || lim < kTreeKeys) {
           if (lim < kTreeKeys) see = (1ull << lim) - 1ull;
           if (blk) see &= words[bt];
-          if (!(g.two && st)) {
-            // thread r < 64 looks after key r: V rows that nobody may see become zero, and values that
-            // are not finite leave the product
-            const uint32_t pos = base + tree_pos_v(k, g.two ? 2 : 4, nt), s = pos % S::kStages;
-            if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && r < kTreeKeys) {
-              uint8_t* vr = ring + s * S::kTile + r * 128;
-              bool bad = false;
-#pragma unroll 1
-              for (int q = 0; q < 8 * kHalves; ++q) {
-                uint4* p = reinterpret_cast<uint4*>(vr + (q >> 3) * kHalf + (q & 7) * 16);
-                if (r >= lim) {
-                  *p = make_uint4(0u, 0u, 0u, 0u);
-                } else if (blk) {
-                  const uint4 x = *p;
-                  if (!(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
-                        tree_finite<BF16>(x.w))) {
-                    bad = true;
-                    uint16_t* half = reinterpret_cast<uint16_t*>(p);
-                    for (int i = 0; i < 8; ++i)
-                      if (!tree_finite<BF16>(half[i])) half[i] = 0;
-                  }
-                }
-              }
-              if (bad) {
-                const int j = bt * kTreeKeys + r;
-                atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
-                ms.bad_any = 1;
-              }
-              fence_proxy_async_smem();
-            }
-          }
         }
         if (ok) ok = mbar_wait(&ms.s_full[2 * st + buf], (cnt >> 1) & 1, a.status);
         ok = __all_sync(0xffffffffu, ok);
+        if (blk || lim < kTreeKeys) {
+          // thread r < 64 looks after key r: V rows that nobody may see become zero, and values that are not
+          // finite are marked and leave the product. With two streams on the tile both do it: each one's
+          // products follow its own pass, and the later one finds values already marked
+          const uint32_t pos = base + tree_pos_v(k, g.two ? 2 : 4, nt), s = pos % S::kStages;
+          if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && r < kTreeKeys) {
+            uint4* vr = reinterpret_cast<uint4*>(ring + s * S::kTile + r * 128);
+            bool bad = false;
+            if (r < lim && blk) {
+#pragma unroll
+              for (int q = 0; q < 8 * kHalves; ++q) {
+                const uint4 x = vr[(q >> 3) * (kHalf / 16) + (q & 7)];
+                bad = bad || !(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
+                               tree_finite<BF16>(x.w));
+              }
+            }
+            if (bad) {
+              const int j = bt * kTreeKeys + r;
+              atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
+              ms.bad_any = 1;
+              __threadfence_block();
+#pragma unroll 1
+              for (int q = 0; q < 8 * kHalves; ++q) {
+                uint16_t* half = reinterpret_cast<uint16_t*>(vr + (q >> 3) * (kHalf / 16) + (q & 7));
+                for (int i = 0; i < 8; ++i)
+                  if (!tree_finite<BF16>(half[i])) half[i] = 0;
+              }
+            }
+            if (r >= lim) {
+#pragma unroll
+              for (int q = 0; q < 8 * kHalves; ++q) vr[(q >> 3) * (kHalf / 16) + (q & 7)] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
         if (ok && warp_ok) {
           tc_fence_after();
           float v[64];
