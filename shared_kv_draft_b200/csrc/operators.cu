@@ -28,9 +28,15 @@ orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap
   if (launch(tree_attention_kernel<D, BF16>, dim3(sms), dim3(kTreeThreads), TreeSmem<D>::kBytes, st, m[0], m[1], m[2],
              m[3], m[4], a) != cudaSuccess)
     return ORTHRUS_ERR_CUDA;
+  // no unit is cut where units and keys are few enough for the even division with one part a unit
+  const int units = a.B * a.Hkv * ((a.N * a.G + kTreeRows - 1) / kTreeRows);
+  const int tiles = (a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
+  if (units <= sms && tiles <= kTreeMinTiles && tiles * kTreeCost2 <= kTreeSwitch) return ORTHRUS_OK;
   const int rows = std::min(kTreeRows, a.N * a.G);
-  return launch(tree_combine_kernel, dim3(sms - 1, (rows + 31) / 32, D / 32), dim3(kJoinThreads), 0, st, a) ==
-                 cudaSuccess
+  const dim3 grid(std::min(sms - 1, units), (rows + 31) / 32);
+  // few CTAs: the columns of a row over several
+  const unsigned int z = grid.x * grid.y >= 2u * sms ? 1 : D / 32;
+  return launch(tree_combine_kernel, dim3(grid.x, grid.y, z), dim3(kJoinThreads), 0, st, a, sms) == cudaSuccess
              ? ORTHRUS_OK
              : ORTHRUS_ERR_CUDA;
 }
@@ -50,7 +56,7 @@ orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* wo
   const CUtensorMapDataType dt = a.bf16 ? kBF16 : kF16;
   const uint64_t z = (uint64_t)a.B * a.Hkv;
   CUtensorMap m[5];
-  const bool ok = map2d(&m[0], a.q, a.d, z * a.N * a.G, 64, 128, dt) &&
+  const bool ok = map2d(&m[0], a.q, a.d, z * a.N * a.G, 64, 32, dt) &&
                   map3d(&m[1], a.k_cache, a.d, a.cap, z, kTreeKeys, 1, dt) &&
                   map3d(&m[2], a.v_cache, a.d, a.cap, z, kTreeKeys, 1, dt) &&
                   map3d(&m[3], a.k_blk, a.d, a.blk_stride, z, kTreeKeys, 1, dt) &&

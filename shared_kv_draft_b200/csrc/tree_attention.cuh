@@ -62,16 +62,11 @@ struct TreeSmem {
   static constexpr int kBytes = 1024 + kMisc + 2048;  // 1024: alignment of the dynamic part
 };
 
-struct TreeStart {  // where a CTA's work starts
-  int scan[kTreeThreads / 32], b, off;
-};
-
 struct TreeMisc {
   uint64_t full[20], empty[20], q_full, q_empty, s_full[4], p_full[4], o_done[2], done[2], seg_done;  // s_full, p_full: 2 stream + buffer
   uint32_t tmem;
   int bad_any;
   unsigned int bad[8];  // tree rows with values that are not finite (this segment)
-  TreeStart start;
   float2 ml[128];       // one stream's (reference, sum) for the other
 };
 static_assert(sizeof(TreeMisc) <= 2048, "misc area");
@@ -124,81 +119,62 @@ struct TreeShare {
   }
 };
 
-// Sum over the CTA's threads, and of those before this one.
-__device__ __forceinline__ int tree_scan(TreeStart& st, int own, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) st.scan[warp] = inc;
-  __syncthreads();
-  int at = inc - own;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kTreeThreads / 32; ++w) {
-    if (w < warp) at += st.scan[w];
-    total += st.scan[w];
-  }
-  return at;
+// The sequence of this lane among 32 from `base` on; empty past the last.
+__device__ __forceinline__ TreeSeq tree_lane_seq(const TreeAttnArgs& a, int base) {
+  TreeSeq s;
+  s.n = s.live = s.tiles = s.groups = s.big = 0;
+  const int b = base + (threadIdx.x & 31);
+  return b < a.B ? TreeSeq(a, b) : s;
 }
 
-// Finds the division, and where CTA c starts in it: sequence st.b (-1: nothing to do) and the cost
-// (line) or part (even) st.off among that sequence's. Called by all threads of the CTA, which
-// hold contiguous shares of the sequences.
-__device__ __forceinline__ TreeShare tree_start(const TreeAttnArgs& a, TreeStart& st, int c, int sms) {
-  const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
-  const int lo = min(a.B, (int)threadIdx.x * per), hi = min(a.B, lo + per);
-  int own = 0, units = 0;
-  for (int b = lo; b < hi; ++b) {
-    const TreeSeq s(a, b);
-    own += s.head() * a.Hkv;
-    units += s.groups * a.Hkv;
-    const int n = a.len[b];
-    if (c == 0 && (n < 0 || n > a.cap)) set_status(a.status, n < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
-  }
-  if (threadIdx.x == 0) st.b = -1;
+// Finds the division, and where CTA c starts in it: sequence b (-1: nothing to do) and the cost
+// (line) or part (even) `off` among that sequence's. Every warp finds them by itself, a lane for a
+// sequence, so that the start of the kernel has no barrier to wait at.
+__device__ __forceinline__ TreeShare tree_start(const TreeAttnArgs& a, int c, int sms, int& b, int& off) {
+  const int lane = threadIdx.x & 31;
+  const TreeSeq first = tree_lane_seq(a, 0);
   TreeShare d;
-  int at = tree_scan(st, own, d.total);
+  d.total = 0;
+  for (int base = 0; base < a.B; base += 32) {
+    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
+    d.total += __reduce_add_sync(0xffffffffu, s.head() * a.Hkv);
+  }
   d.ctas = max(1, min(sms, d.total / kTreeCost2));
   d.each = d.total / d.ctas;
   d.more = d.total - d.each * d.ctas;
   d.per_cost = (float)sms / (float)max(1, d.total);
-  int parts = 0;
-  bool even = true;
-  for (int b = lo; b < hi; ++b) {
-    const TreeSeq s(a, b);
-    parts += d.head_parts(s) * a.Hkv;
-    even = even && d.largest(s) <= d.each + kTreeSwitch;
+  d.even = true;
+  int all = 0;
+  for (int base = 0; d.even && base < a.B; base += 32) {
+    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
+    all += __reduce_add_sync(0xffffffffu, d.head_parts(s) * a.Hkv);
+    d.even = __all_sync(0xffffffffu, d.largest(s) <= d.each + kTreeSwitch) && all <= sms;
   }
-  even = __syncthreads_and(even && units <= sms);
-  d.even = even;
-  if (even) {  // with at most as many parts as CTAs
-    int all;
-    const int before = tree_scan(st, parts, all);
-    d.even = all <= sms;
-    if (d.even) {
-      own = parts;
-      at = before;
-      d.ctas = all;
-    }
-  }
+  if (d.even) d.ctas = all;
   const int mine = d.even ? c : d.at(c);
-  if (c < d.ctas && mine >= at && mine < at + own) {
-    for (int b = lo;; ++b) {
-      const TreeSeq s(a, b);
-      const int w = (d.even ? d.head_parts(s) : s.head()) * a.Hkv;
-      if (mine < at + w) {
-        st.b = b;
-        st.off = mine - at;
-        break;
-      }
-      at += w;
+  int at = 0;
+  b = -1;
+  off = 0;
+  if (c >= d.ctas) return d;
+  for (int base = 0; base < a.B; base += 32) {
+    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
+    const int own = (d.even ? d.head_parts(s) : s.head()) * a.Hkv;
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
     }
+    const int r = mine - at - (inc - own);
+    const unsigned int hit = __ballot_sync(0xffffffffu, r >= 0 && r < own);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = base + src;
+      off = __shfl_sync(0xffffffffu, r, src);
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, inc, 31);
   }
-  __syncthreads();
   return d;
 }
 
@@ -215,9 +191,9 @@ struct TreeWalk {
   int b, kvh, rg, t, t1, c, left;  // left: the range's cost from the unit's start on (line)
   int part, parts;                 // of the unit (even)
   bool first;
-  __device__ TreeWalk(const TreeAttnArgs& a, const TreeShare& d, const TreeStart& st, int c_) {
+  __device__ TreeWalk(const TreeAttnArgs& a, const TreeShare& d, int c_, int b_, int off) {
     c = c_;
-    b = st.b;
+    b = b_;
     first = true;
     left = 0;
     part = 0;
@@ -225,14 +201,14 @@ struct TreeWalk {
     if (b < 0) return;
     s = TreeSeq(a, b);
     const int head = d.even ? d.head_parts(s) : s.head();
-    kvh = st.off / head;
-    int r = st.off - kvh * head;
-    const int n = d.even ? parts_of(d, 0) : s.tiles * s.cost(0);  // of a unit, all but the last
+    kvh = off / head;
+    int r = off - kvh * head;
+    const int n = d.even ? d.parts(s, 0) : s.tiles * s.cost(0);  // of a unit, all but the last
     rg = min(r / n, s.groups - 1);
     r -= rg * n;
     if (d.even) {
       part = r;
-      parts = parts_of(d, rg);
+      parts = d.parts(s, rg);
       t = s.tiles * part / parts;
       t1 = s.tiles * (part + 1) / parts;
       left = 1;
@@ -247,7 +223,6 @@ struct TreeWalk {
       }
     }
   }
-  __device__ int parts_of(const TreeShare& d, int g) const { return d.parts(s, g); }
   __device__ bool next(const TreeAttnArgs& a, TreeSeg& g) {
     if (left <= 0) return false;
     if (parts == 0) {
@@ -468,11 +443,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
   griddep_wait();  // lengths, masks, q and K/V come from earlier kernels
   griddep_launch();
+  int first_b, first_off;
+  const TreeShare share = tree_start(a, blockIdx.x, gridDim.x, first_b, first_off);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.B; b += kTreeThreads)
+      if (a.len[b] < 0 || a.len[b] > a.cap) set_status(a.status, a.len[b] < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
   tc_fence_before();
-  const TreeShare share = tree_start(a, ms.start, blockIdx.x, gridDim.x);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  TreeWalk walk(a, share, ms.start, blockIdx.x);
+  TreeWalk walk(a, share, blockIdx.x, first_b, first_off);
   TreeSeg g;
 
   if (warp == kTreeLoadWarp) {
@@ -481,12 +461,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmKb);
+      tma_prefetch_desc(&tmVb);
       TreeRing<S::kStages> at;
       uint32_t seg = 0;
       bool ok = true;
       while (ok && walk.next(a, g)) {
         const int z = g.b * a.Hkv + g.kvh;
-        const int qtiles = g.two ? 2 : 1, ahead = min(g.two ? 2 : 4, g.t1 - g.t0);
+        const int pieces = (min(kTreeRows, g.live * a.G - g.rg * kTreeRows) + 31) / 32;  // of q, 32 rows each
+        const int ahead = min(g.two ? 2 : 4, g.t1 - g.t0);
         const int ct = (g.n + kTreeKeys - 1) / kTreeKeys;
         auto load = [&](int t, const CUtensorMap* cache, const CUtensorMap* tree) {
           if (!mbar_wait(&ms.empty[at.s], at.phase ^ 1u, a.status)) return false;
@@ -504,11 +487,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int t = g.t0; ok && t < g.t0 + ahead; ++t) ok = load(t, &tmK, &tmKb);
         if (ok && seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
         if (!ok) break;
-        mbar_arrive_expect_tx(&ms.q_full, qtiles * S::kQTile);
+        // rows of the 128-row tiles past the last piece keep what they hold: no sum of another row sees them
+        mbar_arrive_expect_tx(&ms.q_full, pieces * (S::kQTile / 4));
         const int qrow = z * a.N * a.G + g.rg * kTreeRows;
-        for (int h = 0; h < qtiles; ++h)
+        for (int h = 0; h < pieces; ++h)
           for (int e = 0; e < kHalves; ++e)
-            tma_load_2d(sQ + h * S::kQTile + e * kQHalf, &tmQ, &ms.q_full, e * 64, qrow + h * 128);
+            tma_load_2d(sQ + (h >> 2) * S::kQTile + e * kQHalf + (h & 3) * (kQHalf / 4), &tmQ, &ms.q_full, e * 64,
+                        qrow + h * 32);
         ++seg;
         for (int t = g.t0; ok && t < g.t1; ++t) {
           ok = load(t, &tmV, &tmVb);
@@ -638,9 +623,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool warp_ok = lrow - lane < unit_rows;                    // the warp has a row
       const int row = g.rg * kTreeRows + lrow;
       const unsigned long long* words = a.mask + ((size_t)g.b * a.N + (row_ok ? row / a.G : 0)) * a.words;
+      // the word of the segment's first tree tile of this stream, ahead of its use
+      const int ahead = g.two ? 2 : 4, every = g.two ? 1 : 2, k0 = g.two ? 0 : st;
+      int kb = max(k0, ct - g.t0);
+      kb += (kb - k0) & (every - 1);
+      unsigned long long word = kb < nt ? words[kb + g.t0 - ct] : 0ull;
       float m = -INFINITY, l = 0.f;
       bool first = true;
-      for (int k = g.two ? 0 : st; k < nt; k += g.two ? 1 : 2) {
+      for (int k = k0; k < nt; k += every) {
         const int t = g.t0 + k, bt = t - ct;
         const bool blk = t >= ct;
         const int lim = blk ? g.live - bt * kTreeKeys : g.n - t * kTreeKeys;  // keys of the tile, if below 64
@@ -648,15 +638,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         unsigned long long see = ~0ull;
         if (blk || lim < kTreeKeys) {
           if (lim < kTreeKeys) see = (1ull << lim) - 1ull;
-          if (blk) see &= words[bt];
+          if (blk) {
+            see &= word;
+            if (k + every < nt) word = words[bt + every];
+          }
         }
         if (ok) ok = mbar_wait(&ms.s_full[2 * st + buf], (cnt >> 1) & 1, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (blk || lim < kTreeKeys) {
           // thread r < 64 looks after key r: V rows that nobody may see become zero, and values that are not
           // finite are marked and leave the product. With two streams on the tile both do it: each one's
-          // products follow its own pass, and the later one finds values already marked
-          const uint32_t pos = base + tree_pos_v(k, g.two ? 2 : 4, nt), s = pos % S::kStages;
+          // products follow its own pass, and the later one finds values already marked. A row is 128 bytes
+          // of each half: the threads start at different 16 bytes of theirs, on different banks
+          const uint32_t pos = base + tree_pos_v(k, ahead, nt), s = pos % S::kStages;
           if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
           if (ok && r < kTreeKeys) {
@@ -665,7 +659,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (r < lim && blk) {
 #pragma unroll
               for (int q = 0; q < 8 * kHalves; ++q) {
-                const uint4 x = vr[(q >> 3) * (kHalf / 16) + (q & 7)];
+                const uint4 x = vr[(q >> 3) * (kHalf / 16) + ((q + r) & 7)];
                 bad = bad || !(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
                                tree_finite<BF16>(x.w));
               }
@@ -684,7 +678,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             if (r >= lim) {
 #pragma unroll
-              for (int q = 0; q < 8 * kHalves; ++q) vr[(q >> 3) * (kHalf / 16) + (q & 7)] = make_uint4(0u, 0u, 0u, 0u);
+              for (int q = 0; q < 8 * kHalves; ++q) vr[(q >> 3) * (kHalf / 16) + ((q + r) & 7)] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
           }
@@ -844,64 +838,56 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // ---- joining the parts of a cut unit ---------------------------------------------------------
 
-// CTA x reads note x + 1: where that range is the second of a cut unit, it joins 32 rows x 32
-// columns of the unit's parts, thread = (row, 4 columns), in key order:
-//     out = sum_c w_c O_c / sum_c w_c l_c,   w_c = 2^(m_c - max m).
-// The parts' weights are computed once for a row, by the 8 threads that share it.
+// CTA x takes the x-th of the notes that name a cut unit, and joins 32 rows x 32 columns of its
+// parts, thread = (row, 4 columns), in key order:
+//     out = sum_c w_c O_c / sum_c w_c l_c,   w_c = 2^(m_c - max m),
+// eight parts at a time with a running maximum, their loads all in flight together. Bound by the
+// latency of three dependent loads from L2 (notes, parts, and the wait for the first kernel).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 64;  // parts whose weights are held at a time
+constexpr int kJoinParts = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a) {
-  __shared__ float w[kJoinParts][32];
-  __shared__ float red[8][32];
-  griddep_wait();
-  griddep_launch();
-  const int4 note = __ldcg(&a.note[blockIdx.x + 1]);
-  if (note.x < 0) return;
-  const int r = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const int live = a.n_nodes ? min(max(a.n_nodes[note.x], 0), a.N) : a.N;
-  const int lrow = blockIdx.y * 32 + r, rows = live * a.G - note.z * kTreeRows;
-  if ((int)blockIdx.y * 32 >= rows) return;
-  const int c0 = blockIdx.x, n = note.w - c0 + 1;
-  // slot of part i: a range that starts inside the unit uses its CTA's first slot
-  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
+__device__ __forceinline__ void tree_join(const TreeAttnArgs& a, const int4& note, int c0, int n, int lrow, int rows,
+                                          int e4) {
   const float2* ml = a.part_ml + lrow;
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int i = part; i < n; i += 8) top = fmaxf(top, __ldcg(ml + slot(i) * kTreeRows).x);
-  red[part][r] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i][r]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  const int e4 = blockIdx.z * 8 + part;
   const float4* po = a.part_o + (size_t)e4 * kTreeRows + lrow;
-  float l = 0.f;
+  float top = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += kJoinParts) {
-    const int cnt = min(kJoinParts, n - i0);
-    __syncthreads();
-    for (int i = part; i < cnt; i += 8) {
-      const float2 x = __ldcg(ml + slot(i0 + i) * kTreeRows);
-      w[i][r] = exp2f(x.x - ref);
-      l += x.y * w[i][r];
+    float2 m[kJoinParts];
+    float4 x[kJoinParts];
+#pragma unroll
+    for (int i = 0; i < kJoinParts; ++i) {
+      m[i] = make_float2(-INFINITY, 0.f);
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < n) {
+        // slot of part i: all but the first start inside the unit and use their CTA's first slot
+        const size_t slot = (size_t)(2 * (c0 + i0 + i) + (i0 + i == 0 ? 1 : 0));
+        m[i] = __ldcg(ml + slot * kTreeRows);
+        x[i] = __ldcg(po + slot * (a.d / 4) * kTreeRows);
+      }
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int i = 0; i < cnt; ++i) {
-      const float4 x = __ldcg(po + slot(i0 + i) * (a.d / 4) * kTreeRows);
-      const float f = w[i][r];
-      o.x += x.x * f;
-      o.y += x.y * f;
-      o.z += x.z * f;
-      o.w += x.w * f;
+    float next = top;
+#pragma unroll
+    for (int i = 0; i < kJoinParts; ++i) next = fmaxf(next, m[i].x);
+    const float ref = next == -INFINITY ? 0.f : next, f = exp2f(top - ref);
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    top = next;
+#pragma unroll
+    for (int i = 0; i < kJoinParts; ++i) {
+      if (i0 + i < n) {
+        const float w = exp2f(m[i].x - ref);
+        l += m[i].y * w;
+        o.x += x[i].x * w;
+        o.y += x[i].y * w;
+        o.z += x[i].z * w;
+        o.w += x[i].w * w;
+      }
     }
   }
-  red[part][r] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) l += red[i][r];
   if (lrow >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t to = tree_out_at(a, note.x, note.y, note.z * kTreeRows + lrow) + e4 * 4;
@@ -917,6 +903,38 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAt
     *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(h0, h1);
     *reinterpret_cast<uint2*>((uint16_t*)a.out + a.out_lo + to) = make_uint2(l0, l1);
   }
+}
+
+__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a, int sms) {
+  __shared__ int found, before[kJoinThreads / 32];
+  const int r = threadIdx.x & 31, part = threadIdx.x >> 5;
+  if (threadIdx.x == 0) found = -1;
+  griddep_wait();
+  griddep_launch();
+  const int mine = threadIdx.x + 1;
+  for (int c = mine, left = blockIdx.x; c - (int)threadIdx.x < sms; c += kJoinThreads) {  // one lap for up to 257 CTAs
+    const bool cut = c < sms && __ldcg(&a.note[c]).x >= 0;
+    const unsigned int bal = __ballot_sync(0xffffffffu, cut);
+    __syncthreads();
+    if (r == 0) before[part] = __popc(bal);
+    __syncthreads();
+    int at = __popc(bal & ((1u << r) - 1u)), all = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < part) at += before[w];
+      all += before[w];
+    }
+    if (cut && at == left) found = c;
+    left -= all;
+  }
+  __syncthreads();
+  if (found < 0) return;
+  const int4 note = __ldcg(&a.note[found]);
+  const int lrow = blockIdx.y * 32 + r;
+  const int live = a.n_nodes ? min(max(a.n_nodes[note.x], 0), a.N) : a.N;
+  const int rows = live * a.G - note.z * kTreeRows;
+  if ((int)blockIdx.y * 32 >= rows) return;
+  const int c0 = found - 1, n = note.w - c0 + 1;
+  for (int e4 = blockIdx.z * 8 + part; e4 < a.d / 4; e4 += 8 * gridDim.z) tree_join(a, note, c0, n, lrow, rows, e4);
 }
 
 }  // namespace orthrus
