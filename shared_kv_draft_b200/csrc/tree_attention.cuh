@@ -80,10 +80,12 @@ constexpr int kTreeMinTiles = 4;               // tiles of a part at least, in t
 struct TreeSeq {
   int n, live, tiles, groups, big;  // clamped length, nodes, tiles of a unit, row groups, groups of more than 128 rows
   __device__ TreeSeq() {}
-  __device__ TreeSeq(const TreeAttnArgs& a, int b) {
-    n = min(max(a.len[b], 0), a.cap);
-    live = a.n_nodes ? min(max(a.n_nodes[b], 0), a.N) : a.N;
-    const int rows = live * a.G;
+  __device__ TreeSeq(const TreeAttnArgs& a, int b)
+      : TreeSeq(a.G, min(max(a.len[b], 0), a.cap), a.n_nodes ? min(max(a.n_nodes[b], 0), a.N) : a.N) {}
+  __device__ TreeSeq(int G, int n_, int live_) {
+    n = n_;
+    live = live_;
+    const int rows = live * G;
     groups = (rows + kTreeRows - 1) / kTreeRows;
     big = (rows + kTreeRows - 129) / kTreeRows;
     tiles = (n + kTreeKeys - 1) / kTreeKeys + (live + kTreeKeys - 1) / kTreeKeys;
@@ -127,57 +129,6 @@ __device__ __forceinline__ TreeSeq tree_lane_seq(const TreeAttnArgs& a, int base
   return b < a.B ? TreeSeq(a, b) : s;
 }
 
-// Finds the division, and where CTA c starts in it: sequence b (-1: nothing to do) and the cost
-// (line) or part (even) `off` among that sequence's. Every warp finds them by itself, a lane for a
-// sequence, so that the start of the kernel has no barrier to wait at.
-__device__ __forceinline__ TreeShare tree_start(const TreeAttnArgs& a, int c, int sms, int& b, int& off) {
-  const int lane = threadIdx.x & 31;
-  const TreeSeq first = tree_lane_seq(a, 0);
-  TreeShare d;
-  d.total = 0;
-  for (int base = 0; base < a.B; base += 32) {
-    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
-    d.total += __reduce_add_sync(0xffffffffu, s.head() * a.Hkv);
-  }
-  d.ctas = max(1, min(sms, d.total / kTreeCost2));
-  d.each = d.total / d.ctas;
-  d.more = d.total - d.each * d.ctas;
-  d.per_cost = (float)sms / (float)max(1, d.total);
-  d.even = true;
-  int all = 0;
-  for (int base = 0; d.even && base < a.B; base += 32) {
-    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
-    all += __reduce_add_sync(0xffffffffu, d.head_parts(s) * a.Hkv);
-    d.even = __all_sync(0xffffffffu, d.largest(s) <= d.each + kTreeSwitch) && all <= sms;
-  }
-  if (d.even) d.ctas = all;
-  const int mine = d.even ? c : d.at(c);
-  int at = 0;
-  b = -1;
-  off = 0;
-  if (c >= d.ctas) return d;
-  for (int base = 0; base < a.B; base += 32) {
-    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
-    const int own = (d.even ? d.head_parts(s) : s.head()) * a.Hkv;
-    int inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    const int r = mine - at - (inc - own);
-    const unsigned int hit = __ballot_sync(0xffffffffu, r >= 0 && r < own);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      b = base + src;
-      off = __shfl_sync(0xffffffffu, r, src);
-      break;
-    }
-    at += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return d;
-}
-
 // The part of a unit that one CTA works on: tiles [t0, t1) of `tiles`.
 struct TreeSeg {
   int b, kvh, rg, n, live, tiles, t0, t1, slot;
@@ -191,21 +142,20 @@ struct TreeWalk {
   int b, kvh, rg, t, t1, c, left;  // left: the range's cost from the unit's start on (line)
   int part, parts;                 // of the unit (even)
   bool first;
-  __device__ TreeWalk(const TreeAttnArgs& a, const TreeShare& d, int c_, int b_, int off) {
+  __device__ void none() { left = part = parts = 0; }
+  // from the part or the cost `off` of sequence b on
+  __device__ void begin(const TreeShare& d, const TreeSeq& it, int c_, int b_, int off) {
+    s = it;
     c = c_;
     b = b_;
     first = true;
-    left = 0;
-    part = 0;
-    parts = d.even ? 1 : 0;
-    if (b < 0) return;
-    s = TreeSeq(a, b);
     const int head = d.even ? d.head_parts(s) : s.head();
     kvh = off / head;
     int r = off - kvh * head;
     const int n = d.even ? d.parts(s, 0) : s.tiles * s.cost(0);  // of a unit, all but the last
     rg = min(r / n, s.groups - 1);
     r -= rg * n;
+    part = parts = 0;
     if (d.even) {
       part = r;
       parts = d.parts(s, rg);
@@ -258,6 +208,58 @@ struct TreeWalk {
     return true;
   }
 };
+
+// Finds the division, and the start of CTA c's work in it. Every warp finds them by itself, a lane
+// for a sequence, so that the start of the kernel has no barrier to wait at.
+__device__ __forceinline__ TreeShare tree_start(const TreeAttnArgs& a, int c, int sms, TreeWalk& walk) {
+  const int lane = threadIdx.x & 31;
+  const TreeSeq first = tree_lane_seq(a, 0);
+  TreeShare d;
+  d.total = 0;
+#pragma unroll 1
+  for (int base = 0; base < a.B; base += 32) {
+    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
+    d.total += __reduce_add_sync(0xffffffffu, s.head() * a.Hkv);
+  }
+  d.ctas = max(1, min(sms, d.total / kTreeCost2));
+  d.each = d.total / d.ctas;
+  d.more = d.total - d.each * d.ctas;
+  d.per_cost = (float)sms / (float)max(1, d.total);
+  d.even = true;
+  int all = 0;
+#pragma unroll 1
+  for (int base = 0; d.even && base < a.B; base += 32) {
+    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
+    all += __reduce_add_sync(0xffffffffu, d.head_parts(s) * a.Hkv);
+    d.even = __all_sync(0xffffffffu, d.largest(s) <= d.each + kTreeSwitch) && all <= sms;
+  }
+  if (d.even) d.ctas = all;
+  const int mine = d.even ? c : d.at(c);
+  int at = 0;
+  walk.none();
+  if (c >= d.ctas) return d;
+#pragma unroll 1
+  for (int base = 0; base < a.B; base += 32) {
+    const TreeSeq s = base ? tree_lane_seq(a, base) : first;
+    const int own = (d.even ? d.head_parts(s) : s.head()) * a.Hkv;
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const int r = mine - at - (inc - own);
+    const unsigned int hit = __ballot_sync(0xffffffffu, r >= 0 && r < own);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const TreeSeq it(a.G, __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.live, src));
+      walk.begin(d, it, c, base + src, __shfl_sync(0xffffffffu, r, src));
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return d;
+}
 
 // ---- TMEM helpers of this kernel -----------------------------------------------------------
 
@@ -350,19 +352,6 @@ __device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint
 // A warp's common value, told to the compiler.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// A position in the ring: stage, and the parity of its current lap.
-template <int STAGES>
-struct TreeRing {
-  uint32_t s = 0, phase = 0, laps = 0;
-  __device__ __forceinline__ void step() {
-    if (++s == STAGES) {
-      s = 0;
-      phase ^= 1u;
-      laps = 1;
-    }
-  }
-};
-
 template <bool BF16>
 __device__ __forceinline__ uint32_t tree_pack(float x, float y) {
   if constexpr (BF16) {
@@ -402,6 +391,15 @@ __device__ __forceinline__ size_t tree_out_at(const TreeAttnArgs& a, int b, int 
 
 // ---- the kernel -------------------------------------------------------------------------------
 
+// Waits as in ptx.cuh; what a wait that is not over at once takes is one function for all of them, because
+// this kernel is a few short loops whose time goes to instruction fetches when its code is large.
+__device__ __noinline__ bool tree_wait_on(uint64_t* bar, uint32_t parity, int* status) {
+  return mbar_wait(bar, parity, status);
+}
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, int* status) {
+  return mbar_try_wait(bar, parity) || tree_wait_on(bar, parity, status);
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -416,14 +414,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kHalves = D / 64;
   constexpr int kHalf = kTreeKeys * 128, kQHalf = 128 * 128;  // bytes of 64 columns of a K/V tile, of a q tile
+  constexpr uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
+  constexpr uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
 
+  if (warp == kTreeLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmKb);
+    tma_prefetch_desc(&tmVb);
+  }
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&ms.full[s], 1);
       mbar_init(&ms.empty[s], 2);
     }
     mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 2);
+#pragma unroll 1
     for (int s = 0; s < 4; ++s) {
       mbar_init(&ms.s_full[s], 1);
       mbar_init(&ms.p_full[s], 4);
@@ -443,221 +452,76 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
   griddep_wait();  // lengths, masks, q and K/V come from earlier kernels
   griddep_launch();
-  int first_b, first_off;
-  const TreeShare share = tree_start(a, blockIdx.x, gridDim.x, first_b, first_off);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.B; b += kTreeThreads)
-      if (a.len[b] < 0 || a.len[b] > a.cap) set_status(a.status, a.len[b] < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
+  TreeWalk walk;
+  const TreeShare share = tree_start(a, blockIdx.x, gridDim.x, walk);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  TreeWalk walk(a, share, blockIdx.x, first_b, first_off);
-  TreeSeg g;
 
-  if (warp == kTreeLoadWarp) {
-    // ---- loads: Q of a segment, then K and V of its tiles in the order in which the MMA warp uses them ----
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmKb);
-      tma_prefetch_desc(&tmVb);
-      TreeRing<S::kStages> at;
-      uint32_t seg = 0;
-      bool ok = true;
-      while (ok && walk.next(a, g)) {
-        const int z = g.b * a.Hkv + g.kvh;
-        const int pieces = (min(kTreeRows, g.live * a.G - g.rg * kTreeRows) + 31) / 32;  // of q, 32 rows each
-        const int ahead = min(g.two ? 2 : 4, g.t1 - g.t0);
-        const int ct = (g.n + kTreeKeys - 1) / kTreeKeys;
-        auto load = [&](int t, const CUtensorMap* cache, const CUtensorMap* tree) {
-          if (!mbar_wait(&ms.empty[at.s], at.phase ^ 1u, a.status)) return false;
-          mbar_arrive_expect_tx(&ms.full[at.s], S::kTile);
-          const bool blk = t >= ct;
-          const CUtensorMap* m = blk ? tree : cache;
-          const int y = (blk ? t - ct : t) * kTreeKeys;
-          uint8_t* dst = ring + at.s * S::kTile;
-#pragma unroll
-          for (int e = 0; e < kHalves; ++e) tma_load_3d(dst + e * kHalf, m, &ms.full[at.s], e * 64, y, z);
-          at.step();
-          return true;
-        };
-        // the first K tiles fill free stages while the last segment's scores still read its q
-        for (int t = g.t0; ok && t < g.t0 + ahead; ++t) ok = load(t, &tmK, &tmKb);
-        if (ok && seg > 0) ok = mbar_wait(&ms.q_empty, (seg - 1) & 1, a.status);
-        if (!ok) break;
-        // rows of the 128-row tiles past the last piece keep what they hold: no sum of another row sees them
-        mbar_arrive_expect_tx(&ms.q_full, pieces * (S::kQTile / 4));
-        const int qrow = z * a.N * a.G + g.rg * kTreeRows;
-        for (int h = 0; h < pieces; ++h)
-          for (int e = 0; e < kHalves; ++e)
-            tma_load_2d(sQ + (h >> 2) * S::kQTile + e * kQHalf + (h & 3) * (kQHalf / 4), &tmQ, &ms.q_full, e * 64,
-                        qrow + h * 32);
-        ++seg;
-        for (int t = g.t0; ok && t < g.t1; ++t) {
-          ok = load(t, &tmV, &tmVb);
-          if (ok && t + ahead < g.t1) ok = load(t + ahead, &tmK, &tmKb);
-        }
-      }
-      // copies in flight land before the CTA ends: the last use of each stage
-      if (seg > 0) mbar_wait(&ms.q_full, (seg - 1) & 1, a.status);
-      for (int k = 0; k < S::kStages; ++k) {
-        if (at.laps > 0 || k < (int)at.s) mbar_wait(&ms.full[k], k < (int)at.s ? at.phase : at.phase ^ 1u, a.status);
-      }
-    }
-  } else if (warp == kTreeMmaWarp || warp == kTreeMmaWarp + 1) {
-    // ---- products: S = Q K^T, two jobs of a stream ahead of O += P V. With more than 128 rows the streams
-    // have a warp each (the instruction latency of this loop, not the products, would otherwise set the
-    // pace) and a stage is free after a commit of each; else the first warp serves both streams, sees every
-    // stage in order, and commits twice. The whole warp runs the loop on warp-uniform values, one elected
-    // thread issues ----
-    constexpr uint32_t idS = BF16 ? idesc_bf16(128, kTreeKeys, false) : idesc_f16(128, kTreeKeys, false);
-    constexpr uint32_t idO = BF16 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
-    const bool issue = elect_one();
-    const uint32_t mine = warp - kTreeMmaWarp;
-    const uint32_t r_desc = uniform(smem_u32(ring) >> 4), q_desc = uniform(smem_u32(sQ) >> 4), tm = uniform(tmem);
-    uint32_t base = 0, seg = 0, c0 = 0, c1 = 0;  // ring position of the segment; segments, jobs of each stream so far
-    bool ok = true, was_two = false;
-    while (ok && walk.next(a, g)) {
-      const int nt = uniform(g.t1 - g.t0);
-      const bool two = uniform(g.two);
-      const int ahead = two ? 2 : 4;
-      // seg_done: both warps have issued a segment's products and they are complete. Each warp sees every
-      // phase: before its scores where the streams change hands (the S buffers' last readers were issued by
-      // the other warp), else before its sums
-      const bool early = two != was_two;
-      was_two = two;
-      if (early && seg > 0) ok = mbar_wait(&ms.seg_done, (seg - 1) & 1, a.status);
-      if (two || mine == 0) {
-        if (ok) ok = mbar_wait(&ms.q_full, seg & 1, a.status);
-        const uint32_t qd = q_desc + (two ? mine * (S::kQTile >> 4) : 0);
-        // job of tile k: its stream, and the stream's job number
-        auto stream = [&](int k) { return two ? mine : (uint32_t)k & 1u; };
-        auto job = [&](int k) { return two ? (mine ? c1 : c0) + k : ((k & 1) ? c1 : c0) + (k >> 1); };
-        auto scores = [&](int k) {
-          const uint32_t pos = base + tree_pos_k(k, ahead), s = pos % S::kStages, buf = 2 * stream(k) + (job(k) & 1u);
-          if (!mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status)) return false;
-          tc_fence_after();
-          const uint32_t to = tm + buf * 64, kd = r_desc + s * (S::kTile >> 4);
-          if (issue) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              mma_ss_lo(to, qd + (((i >> 2) * kQHalf + (i & 3) * 32) >> 4), kd + (((i >> 2) * kHalf + (i & 3) * 32) >> 4), 16,
-                        idS, i > 0 ? 1u : 0u);
-            mma_commit(&ms.s_full[buf]);
-            mma_commit(&ms.empty[s]);
-            if (!two) mma_commit(&ms.empty[s]);
-            if (k == nt - 1) {
-              mma_commit(&ms.q_empty);
-              if (!two) mma_commit(&ms.q_empty);
-            }
-          }
-          return true;
-        };
-        for (int k = 0; ok && k < ahead && k < nt; ++k) ok = scores(k);
-        if (ok && !early && seg > 0) ok = mbar_wait(&ms.seg_done, (seg - 1) & 1, a.status);
-        for (int k = 0; ok && k < nt; ++k) {
-          const uint32_t pos = base + tree_pos_v(k, ahead, nt), s = pos % S::kStages;
-          const uint32_t st = stream(k), n = job(k), buf = 2 * st + (n & 1u);
-          ok = mbar_wait(&ms.p_full[buf], (n >> 1) & 1u, a.status) &&
-               mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t to = tm + 256 + st * 128, from = tm + buf * 64, vd = r_desc + s * (S::kTile >> 4);
-          const uint32_t add = k >= (two ? 1 : 2) ? 1u : 0u;  // the stream's first job of the segment starts its sums
-          if (issue) {
-#pragma unroll
-            for (int i = 0; i < kTreeKeys / 16; ++i)
-              mma_ts_lo(to, from + i * 8, vd + i * (2048 >> 4), kHalf, idO, i > 0 ? 1u : add);
-            mma_commit(&ms.o_done[st]);
-            mma_commit(&ms.empty[s]);
-            if (!two) mma_commit(&ms.empty[s]);
-          }
-          if (k + ahead < nt) ok = scores(k + ahead);
-        }
-        if (ok && issue) mma_commit(&ms.seg_done);
-      } else {
-        if (ok && !early && seg > 0) ok = mbar_wait(&ms.seg_done, (seg - 1) & 1, a.status);
-        if (ok && issue) mbar_arrive(&ms.seg_done);
-      }
-      c0 += two ? nt : (nt + 1) >> 1;
-      c1 += two ? nt : nt >> 1;
-      base += 2 * nt;
-      ++seg;
-    }
-    if (issue) mma_commit(&ms.done[mine]);
-    mbar_wait(&ms.done[mine], 0, a.status);
-  } else if (warp == kTreeNoteWarp) {
-    // ---- for the joining kernel: whether this CTA has the second part of a unit that is cut ----
-    if (lane == 0) {
-      int4 note = make_int4(-1, 0, 0, 0);
-      const int c = blockIdx.x, r = walk.left - (share.at(c + 1) - share.at(c));  // line: the unit's cost before the range
-      if (walk.next(a, g) && g.t0 > 0) {
-        int last = c;
-        if (share.even) {
-          last = walk.part == 1 ? c + walk.parts - 2 : -1;
-        } else {
-          const int u0 = share.at(c) - r, tail = u0 + (g.tiles - 1) * (g.two ? kTreeCost2 : kTreeCost1);
-          if (share.at(c - 1) > u0) last = -1;
-          else
-            while (last + 1 < share.ctas && share.at(last + 1) <= tail) ++last;
-        }
-        if (last >= 0) note = make_int4(g.b, g.kvh, g.rg, last);
-      }
-      a.note[c] = note;
-    }
-  } else if (warp < 8) {
-    // ---- softmax: stream 0 or 1, thread = row ----
-    const int st = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256;
-    const float sl = a.scale_log2;
-    uint32_t base = 0, cnt = 0;
-    bool ok = true;  // after a wait that ran out: no more TMEM accesses, but the same barriers
-    while (walk.next(a, g)) {
-      const int nt = g.t1 - g.t0, ct = (g.n + kTreeKeys - 1) / kTreeKeys;
-      const int unit_rows = g.live * a.G - g.rg * kTreeRows;           // rows from this group on
-      const int lrow = (g.two ? st * 128 : 0) + r;                     // row within the group
+  // of every role: segments, ring position of the segment (tiles go through the ring in the order of
+  // their use: `ahead` tiles of K, then V and K in turn), and a wait that ran out
+  uint32_t seg = 0, base = 0;
+  bool ok = true;
+  // MMA warps: jobs of each stream so far, and the last segment's kind
+  const bool issue = elect_one();
+  const uint32_t mine = warp - kTreeMmaWarp;
+  uint32_t c0 = 0, c1 = 0;
+  bool was_two = false;
+  // softmax: stream, row of the 128, jobs so far
+  const int st = warp >> 2, r = (warp & 3) * 32 + lane;
+  uint32_t cnt = 0;
+  // note warp: the unit's cost before the range (line)
+  const int skipped = walk.left - (share.at(blockIdx.x + 1) - share.at(blockIdx.x));
+  int4 note = make_int4(-1, 0, 0, 0);
+
+  TreeSeg g;
+#pragma unroll 1
+  while (walk.next(a, g)) {
+    const int nt = uniform(g.t1 - g.t0), ct = (g.n + kTreeKeys - 1) / kTreeKeys;
+    const bool two = uniform(g.two);
+    const int ahead = two ? 2 : 4;
+
+    if (warp < 8) {
+      // ---- softmax: thread = row ----
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256;
+      const float sl = a.scale_log2;
+      const int unit_rows = g.live * a.G - g.rg * kTreeRows;  // rows from this group on
+      const int lrow = (two ? st * 128 : 0) + r;              // row within the group
       const bool row_ok = lrow < unit_rows;
-      const bool warp_ok = lrow - lane < unit_rows;                    // the warp has a row
-      const int row = g.rg * kTreeRows + lrow;
-      const unsigned long long* words = a.mask + ((size_t)g.b * a.N + (row_ok ? row / a.G : 0)) * a.words;
+      const bool warp_ok = lrow - lane < unit_rows;           // the warp has a row
+      const int row = g.rg * kTreeRows + lrow, node = row_ok ? row / a.G : 0;
+      const unsigned long long* words = a.mask + ((size_t)g.b * a.N + node) * a.words;
       // the word of the segment's first tree tile of this stream, ahead of its use
-      const int ahead = g.two ? 2 : 4, every = g.two ? 1 : 2, k0 = g.two ? 0 : st;
+      const int every = two ? 1 : 2, k0 = two ? 0 : st;
       int kb = max(k0, ct - g.t0);
       kb += (kb - k0) & (every - 1);
       unsigned long long word = kb < nt ? words[kb + g.t0 - ct] : 0ull;
       float m = -INFINITY, l = 0.f;
-      bool first = true;
+#pragma unroll 1
       for (int k = k0; k < nt; k += every) {
         const int t = g.t0 + k, bt = t - ct;
         const bool blk = t >= ct;
         const int lim = blk ? g.live - bt * kTreeKeys : g.n - t * kTreeKeys;  // keys of the tile, if below 64
         const uint32_t buf = cnt & 1;
-        unsigned long long see = ~0ull;
-        if (blk || lim < kTreeKeys) {
-          if (lim < kTreeKeys) see = (1ull << lim) - 1ull;
-          if (blk) {
-            see &= word;
-            if (k + every < nt) word = words[bt + every];
-          }
-        }
-        if (ok) ok = mbar_wait(&ms.s_full[2 * st + buf], (cnt >> 1) & 1, a.status);
+        if (ok) ok = tree_wait(&ms.s_full[2 * st + buf], (cnt >> 1) & 1, a.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (blk || lim < kTreeKeys) {
+        const bool part = blk || lim < kTreeKeys;
+        if (part) {
           // thread r < 64 looks after key r: V rows that nobody may see become zero, and values that are not
           // finite are marked and leave the product. With two streams on the tile both do it: each one's
           // products follow its own pass, and the later one finds values already marked. A row is 128 bytes
-          // of each half: the threads start at different 16 bytes of theirs, on different banks
+          // of each half: the threads start at different 16 bytes of theirs, on different banks. (The wait is
+          // after that for the scores: then the stage's earlier laps are over, and its parity is this lap's.)
           const uint32_t pos = base + tree_pos_v(k, ahead, nt), s = pos % S::kStages;
-          if (ok) ok = mbar_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+          if (ok) ok = tree_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
           if (ok && r < kTreeKeys) {
             uint4* vr = reinterpret_cast<uint4*>(ring + s * S::kTile + r * 128);
             bool bad = false;
             if (r < lim && blk) {
-#pragma unroll
+#pragma unroll 4
               for (int q = 0; q < 8 * kHalves; ++q) {
                 const uint4 x = vr[(q >> 3) * (kHalf / 16) + ((q + r) & 7)];
                 bad = bad || !(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
@@ -670,14 +534,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               ms.bad_any = 1;
               __threadfence_block();
 #pragma unroll 1
-              for (int q = 0; q < 8 * kHalves; ++q) {
-                uint16_t* half = reinterpret_cast<uint16_t*>(vr + (q >> 3) * (kHalf / 16) + (q & 7));
-                for (int i = 0; i < 8; ++i)
-                  if (!tree_finite<BF16>(half[i])) half[i] = 0;
+              for (int q = 0; q < 64 * kHalves; ++q) {
+                uint16_t* x = reinterpret_cast<uint16_t*>(vr) + (q >> 6) * (kHalf / 2) + (q & 63);
+                if (!tree_finite<BF16>(*x)) *x = 0;
               }
             }
             if (r >= lim) {
-#pragma unroll
+#pragma unroll 4
               for (int q = 0; q < 8 * kHalves; ++q) vr[(q >> 3) * (kHalf / 16) + ((q + r) & 7)] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
@@ -687,8 +550,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tc_fence_after();
           float v[64];
           tmem_ld64(tS + buf * 64, v);
-          if (blk || lim < kTreeKeys) {
-            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+          if (part) {
+            uint32_t s0 = ~0u, s1 = ~0u;
+            if (lim < kTreeKeys) {
+              s0 = lim >= 32 ? ~0u : (1u << lim) - 1u;
+              s1 = lim > 32 ? (1u << (lim - 32)) - 1u : 0u;
+            }
+            if (blk) {
+              s0 &= (uint32_t)word;
+              s1 &= (uint32_t)(word >> 32);
+              if (k + every < nt) word = words[bt + every];
+            }
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               if (!((i < 32 ? s0 >> i : s1 >> (i - 32)) & 1u)) v[i] = -INFINITY;
@@ -699,13 +571,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], v[i + 2 * q], v[i + 2 * q + 1]);
           const float mt = fmaxf(max3(mx[0], mx[1], fmaxf(v[60], v[61])), max3(mx[2], mx[3], fmaxf(v[62], v[63]))) * sl;
-          if (first) {
+          if (k == k0) {
             m = mt;
           } else {
             const bool move = mt > m + kTreeSlack;
             if (__any_sync(0xffffffffu, move)) {
               // the stream's last product is complete before its sums are scaled
-              ok = __all_sync(0xffffffffu, mbar_wait(&ms.o_done[st], (cnt - 1) & 1, a.status));
+              ok = __all_sync(0xffffffffu, tree_wait(&ms.o_done[st], (cnt - 1) & 1, a.status));
               if (ok) {
                 tc_fence_after();
                 const float f = move ? exp2f(m - mt) : 1.f;
@@ -740,20 +612,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&ms.p_full[2 * st + buf]);
-        first = false;
         ++cnt;
       }
-      base += 2 * nt;
 
       // ---- the segment's sums ----
-      const bool mine = g.two || nt > st;  // this stream had a job
       // the last two products may both be under way: one phase after the other
-      if (ok && mine && cnt > 1) ok = mbar_wait(&ms.o_done[st], (cnt - 2) & 1, a.status);
-      if (ok && mine) ok = mbar_wait(&ms.o_done[st], (cnt - 1) & 1, a.status);
+      if (two || nt > st) {
+        if (ok && cnt > 1) ok = tree_wait(&ms.o_done[st], (cnt - 2) & 1, a.status);
+        if (ok) ok = tree_wait(&ms.o_done[st], (cnt - 1) & 1, a.status);
+      }
       ok = __all_sync(0xffffffffu, ok);
-      float w_own = 1.f, w_other = 0.f;
+      float w0 = 1.f, w1 = 0.f;
       int e0 = 0, e1 = D;
-      if (!g.two) {
+      if (!two) {
         // both streams hold sums of the same rows: each joins one half of the columns
         if (st) ms.ml[r] = make_float2(m, l);
         named_bar_sync(1, 256);
@@ -762,60 +633,61 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (!st) ms.ml[r] = make_float2(m, l);
         named_bar_sync(1, 256);
         const float2 ml0 = ms.ml[r];
-        const float top = fmaxf(ml0.x, ml1.x), ref = top == -INFINITY ? 0.f : top;
-        w_own = exp2f(ml0.x - ref);
-        w_other = exp2f(ml1.x - ref);
-        m = top;
-        l = ml0.y * w_own + ml1.y * w_other;
+        m = fmaxf(ml0.x, ml1.x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        w0 = exp2f(ml0.x - ref);
+        w1 = exp2f(ml1.x - ref);
+        l = ml0.y * w0 + ml1.y * w1;
         e0 = st ? D / 2 : 0;
         e1 = st ? D : D / 2;
       }
       bool bad = *(volatile int*)&ms.bad_any != 0;
       if (ok && warp_ok) {
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool whole = g.whole();
-        const size_t at = row_ok ? tree_out_at(a, g.b, g.kvh, row) : 0;
+        if (whole) {  // the quotient's factor into the weights
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          w0 *= inv;
+          w1 *= inv;
+        }
+        const size_t at = (((size_t)g.b * a.N + node) * a.Hkv * a.G + (size_t)g.kvh * a.G + (row - node * a.G)) * D;
         float4* po = a.part_o + (size_t)g.slot * (D / 4) * kTreeRows + lrow;
 #pragma unroll 1
-        for (int e = e0; e < e1; e += 32) {
-          float o[32];
-          if (g.two) {
-            tmem_ld32(tO + st * 128 + e, o);
+        for (int e = e0; e < e1; e += 16) {
+          float o[16], x[16];
+          tmem_ld16(tO + (two ? st * 128 : 0) + e, o);
+          if (!two && nt > 1) {
+            tmem_ld16(tO + 128 + e, x);
           } else {
-            tmem_ld32(tO + e, o);
-            if (nt > 1) {
-              float x[32];
-              tmem_ld32(tO + 128 + e, x);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = o[i] * w_own + x[i] * w_other;
-            }
+            for (int i = 0; i < 16; ++i) x[i] = 0.f;
           }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * w0 + x[i] * w1;
           if (bad && row_ok) {
+#pragma unroll 1
             for (int j = 0; j < g.live; ++j)
               if ((ms.bad[j >> 5] >> (j & 31) & 1u) && (words[j >> 6] >> (j & 63) & 1ull)) {
                 const size_t vat = ((size_t)(g.b * a.Hkv + g.kvh) * a.blk_stride + j) * D + e;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float x = BF16 ? __bfloat162float(((const __nv_bfloat16*)a.v_blk)[vat + i])
+                for (int i = 0; i < 16; ++i) {
+                  const float y = BF16 ? __bfloat162float(((const __nv_bfloat16*)a.v_blk)[vat + i])
                                        : __half2float(((const __half*)a.v_blk)[vat + i]);
-                  if (!isfinite(x)) o[i] += x;
+                  if (!isfinite(y)) o[i] += y;
                 }
               }
           }
           if (!row_ok) continue;
           if (whole) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= inv;
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) tree_store8(a, at + e + i, o + i);
+            tree_store8(a, at + e, o);
+            tree_store8(a, at + e + 8, o + 8);
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
               po[(size_t)(e / 4 + i) * kTreeRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-        if (!whole && row_ok && (g.two || !st)) a.part_ml[(size_t)g.slot * kTreeRows + lrow] = make_float2(m, l);
+        if (!whole && row_ok && (two || !st)) a.part_ml[(size_t)g.slot * kTreeRows + lrow] = make_float2(m, l);
       }
       tc_fence_before();
       bad = named_bar_or(2, 256, bad);  // O and the marks are read before the next segment writes them
@@ -824,8 +696,145 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (threadIdx.x == 0) ms.bad_any = 0;
         named_bar_sync(1, 256);
       }
+    } else if (warp == kTreeLoadWarp) {
+      // ---- loads: K and V in the order of their use, and q when the first K tiles are on their way (they
+      // fill free stages while the last segment's scores still read its q) ----
+      if (lane == 0 && ok) {
+        const int z = g.b * a.Hkv + g.kvh, lead = min(ahead, nt);
+#pragma unroll 1
+        for (int p = 0; p < 2 * nt; ++p) {
+          if (p == lead) {
+            const int pieces = (min(kTreeRows, g.live * a.G - g.rg * kTreeRows) + 31) / 32;  // of q, 32 rows each
+            if (seg > 0 && !(ok = tree_wait(&ms.q_empty, (seg - 1) & 1, a.status))) break;
+            // rows of the 128-row tiles past the last piece keep what they hold: no sum of another row sees them
+            mbar_arrive_expect_tx(&ms.q_full, pieces * (S::kQTile / 4));
+            const int qrow = z * a.N * a.G + g.rg * kTreeRows;
+#pragma unroll 1
+            for (int h = 0; h < pieces; ++h)
+              for (int e = 0; e < kHalves; ++e)
+                tma_load_2d(sQ + (h >> 2) * S::kQTile + e * kQHalf + (h & 3) * (kQHalf / 4), &tmQ, &ms.q_full, e * 64,
+                            qrow + h * 32);
+          }
+          // position p: K first, then V and K in turn, V last
+          const bool val = p >= lead && (p >= 2 * nt - lead || ((p - lead) & 1) == 0);
+          const int k = p < lead ? p : (p >= 2 * nt - lead ? p - nt : (p - lead) / 2 + (val ? 0 : lead));
+          const uint32_t pos = base + p, s = pos % S::kStages, lap = pos / S::kStages;
+          if (!(ok = tree_wait(&ms.empty[s], (lap & 1) ^ 1u, a.status))) break;
+          mbar_arrive_expect_tx(&ms.full[s], S::kTile);
+          const int t = g.t0 + k;
+          const bool blk = t >= ct;
+          const CUtensorMap* map = val ? (blk ? &tmVb : &tmV) : (blk ? &tmKb : &tmK);
+          const int y = (blk ? t - ct : t) * kTreeKeys;
+          uint8_t* dst = ring + s * S::kTile;
+#pragma unroll
+          for (int e = 0; e < kHalves; ++e) tma_load_3d(dst + e * kHalf, map, &ms.full[s], e * 64, y, z);
+        }
+      }
+    } else if (warp <= kTreeMmaWarp + 1) {
+      // ---- products: S = Q K^T, two jobs of a stream ahead of O += P V. With more than 128 rows the streams
+      // have a warp each (the instruction latency of this loop, not the products, would otherwise set the
+      // pace) and a stage is free after a commit of each; else the first warp serves both streams, sees every
+      // stage in order, and commits twice. The whole warp runs the loop on warp-uniform values, one elected
+      // thread issues.
+      // seg_done: both warps have issued a segment's products and they are complete. Each warp sees every
+      // phase: before its scores where the streams change hands (the S buffers' last readers were issued by
+      // the other warp), else before its sums ----
+      const bool early = two != was_two;
+      was_two = two;
+      if (ok && early && seg > 0) ok = tree_wait(&ms.seg_done, (seg - 1) & 1, a.status);
+      if (two || mine == 0) {
+        const uint32_t r_desc = uniform(smem_u32(ring) >> 4), tm = uniform(tmem);
+        const uint32_t qd = uniform(smem_u32(sQ) >> 4) + (two ? mine * (S::kQTile >> 4) : 0);
+        // job of tile k: its stream, and the stream's job number
+        auto stream = [&](int k) { return two ? mine : (uint32_t)k & 1u; };
+        auto job = [&](int k) { return two ? (mine ? c1 : c0) + k : ((k & 1) ? c1 : c0) + (k >> 1); };
+        if (ok) ok = tree_wait(&ms.q_full, seg & 1, a.status);
+#pragma unroll 1
+        for (int k = -ahead; ok && k < nt; ++k) {
+          if (k == 0 && !early && seg > 0 && !(ok = tree_wait(&ms.seg_done, (seg - 1) & 1, a.status))) break;
+          if (k >= 0) {
+            const uint32_t pos = base + tree_pos_v(k, ahead, nt), s = pos % S::kStages;
+            const uint32_t sk = stream(k), n = job(k), buf = 2 * sk + (n & 1u);
+            ok = tree_wait(&ms.p_full[buf], (n >> 1) & 1u, a.status) &&
+                 tree_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t to = tm + 256 + sk * 128, from = tm + buf * 64, vd = r_desc + s * (S::kTile >> 4);
+            const uint32_t add = k >= (two ? 1 : 2) ? 1u : 0u;  // the stream's first job of the segment starts its sums
+            if (issue) {
+#pragma unroll
+              for (int i = 0; i < kTreeKeys / 16; ++i)
+                mma_ts_lo(to, from + i * 8, vd + i * (2048 >> 4), kHalf, idO, i > 0 ? 1u : add);
+              mma_commit(&ms.o_done[sk]);
+              mma_commit(&ms.empty[s]);
+              if (!two) mma_commit(&ms.empty[s]);
+            }
+          }
+          const int kn = k + ahead;
+          if (kn < nt) {
+            const uint32_t pos = base + tree_pos_k(kn, ahead), s = pos % S::kStages;
+            const uint32_t buf = 2 * stream(kn) + (job(kn) & 1u);
+            ok = tree_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t to = tm + buf * 64, kd = r_desc + s * (S::kTile >> 4);
+            if (issue) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+                mma_ss_lo(to, qd + (((i >> 2) * kQHalf + (i & 3) * 32) >> 4), kd + (((i >> 2) * kHalf + (i & 3) * 32) >> 4),
+                          16, idS, i > 0 ? 1u : 0u);
+              mma_commit(&ms.s_full[buf]);
+              mma_commit(&ms.empty[s]);
+              if (!two) mma_commit(&ms.empty[s]);
+              if (kn == nt - 1) {
+                mma_commit(&ms.q_empty);
+                if (!two) mma_commit(&ms.q_empty);
+              }
+            }
+          }
+        }
+        if (ok && issue) mma_commit(&ms.seg_done);
+      } else {
+        if (ok && !early && seg > 0) ok = tree_wait(&ms.seg_done, (seg - 1) & 1, a.status);
+        if (ok && issue) mbar_arrive(&ms.seg_done);
+      }
+      c0 += two ? nt : (nt + 1) >> 1;
+      c1 += two ? nt : nt >> 1;
+    } else if (seg == 0 && g.t0 > 0) {
+      // ---- for the joining kernel: whether this CTA has the second part of a unit that is cut ----
+      const int c = blockIdx.x;
+      int last = c;
+      if (share.even) {
+        last = walk.part == 1 ? c + walk.parts - 2 : -1;
+      } else {
+        const int u0 = share.at(c) - skipped, tail = u0 + (g.tiles - 1) * (two ? kTreeCost2 : kTreeCost1);
+        if (share.at(c - 1) > u0) last = -1;
+        else
+          while (last + 1 < share.ctas && share.at(last + 1) <= tail) ++last;
+      }
+      if (last >= 0) note = make_int4(g.b, g.kvh, g.rg, last);
     }
+    base += 2 * nt;
+    ++seg;
   }
+
+  if (warp == kTreeLoadWarp) {
+    // copies in flight land before the CTA ends: the last use of each stage
+    if (lane == 0 && seg > 0) {
+      tree_wait(&ms.q_full, (seg - 1) & 1, a.status);
+#pragma unroll 1
+      for (uint32_t k = base > S::kStages ? base - S::kStages : 0; k < base; ++k)
+        tree_wait(&ms.full[k % S::kStages], (k / S::kStages) & 1, a.status);
+    }
+  } else if (warp >= kTreeMmaWarp && warp <= kTreeMmaWarp + 1) {
+    if (issue) mma_commit(&ms.done[mine]);
+    tree_wait(&ms.done[mine], 0, a.status);
+  } else if (warp == kTreeNoteWarp && lane == 0) {
+    a.note[blockIdx.x] = note;
+  }
+  if (blockIdx.x == 0 && warp < 8)
+    for (int b = threadIdx.x; b < a.B; b += 256)
+      if (a.len[b] < 0 || a.len[b] > a.cap) set_status(a.status, a.len[b] < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
 
   tc_fence_before();
   __syncthreads();
