@@ -31,14 +31,14 @@ orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap
   // no unit is cut where units and keys are few enough for the even division with one part a unit
   const int units = a.B * a.Hkv * ((a.N * a.G + kTreeRows - 1) / kTreeRows);
   const int tiles = (a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
-  if (units <= sms && tiles <= kTreeMinTiles && tiles * kTreeCost2 <= kTreeSwitch) return ORTHRUS_OK;
-  const int rows = std::min(kTreeRows, a.N * a.G);
-  const dim3 grid(std::min(sms - 1, units), (rows + 31) / 32);
+  if (units <= sms && tiles <= kTreeMinTiles && kTreeUnit + tiles * kTreeCost2 <= kTreeSwitch + kTreeUnit + kTreeCost1)
+    return ORTHRUS_OK;
+  const dim3 grid(std::min(sms - 1, units), (std::min(kTreeRows, a.N * a.G) + 31) / 32);
   // few CTAs: the columns of a row over several
-  const unsigned int z = grid.x * grid.y >= 2u * sms ? 1 : D / 32;
-  return launch(tree_combine_kernel, dim3(grid.x, grid.y, z), dim3(kJoinThreads), 0, st, a, sms) == cudaSuccess
-             ? ORTHRUS_OK
-             : ORTHRUS_ERR_CUDA;
+  const bool spread = (int)(grid.x * grid.y) < sms;
+  const cudaError_t e = spread ? launch(tree_combine_kernel<1>, dim3(grid.x, grid.y, D / 32), dim3(kJoinThreads), 0, st, a, sms)
+                               : launch(tree_combine_kernel<D / 32>, grid, dim3(kJoinThreads), 0, st, a, sms);
+  return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
 }
 
 }  // namespace
@@ -52,7 +52,7 @@ orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* wo
   // the costs of all tiles are counted in 31 bits
   const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
   const long long units = (long long)a.B * a.Hkv * (((long long)a.N * a.G + kTreeRows - 1) / kTreeRows);
-  if (units * tiles > INT32_MAX / kTreeCost2) return ORTHRUS_ERR_UNSUPPORTED;
+  if (units * (kTreeUnit + tiles * kTreeCost2) > INT32_MAX) return ORTHRUS_ERR_UNSUPPORTED;
   const CUtensorMapDataType dt = a.bf16 ? kBF16 : kF16;
   const uint64_t z = (uint64_t)a.B * a.Hkv;
   CUtensorMap m[5];

@@ -74,8 +74,9 @@ static_assert(sizeof(TreeMisc) <= 2048, "misc area");
 // ---- who works on what ------------------------------------------------------------------
 
 constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile's relative time with up to 128 rows, with more
-constexpr int kTreeSwitch = 16;                // and that of a second segment in a CTA
-constexpr int kTreeMinTiles = 4;               // tiles of a part at least, in the even division
+constexpr int kTreeUnit = 8;                   // and that of a unit: pipeline filled and drained, sums stored
+constexpr int kTreeSwitch = 10;                // how much longer than a range the even division's parts may be
+constexpr int kTreeMinTiles = 3;               // even division: tiles of a part at least
 
 struct TreeSeq {
   int n, live, tiles, groups, big;  // clamped length, nodes, tiles of a unit, row groups, groups of more than 128 rows
@@ -91,12 +92,16 @@ struct TreeSeq {
     tiles = (n + kTreeKeys - 1) / kTreeKeys + (live + kTreeKeys - 1) / kTreeKeys;
   }
   __device__ int cost(int rg) const { return rg < big ? kTreeCost2 : kTreeCost1; }  // of a tile
-  __device__ int head() const { return tiles * (big * kTreeCost2 + (groups - big) * kTreeCost1); }  // of a KV head
+  __device__ int unit(int rg) const { return kTreeUnit + tiles * cost(rg); }
+  __device__ int head() const {  // of a KV head
+    return groups * kTreeUnit + tiles * (big * kTreeCost2 + (groups - big) * kTreeCost1);
+  }
 };
 
 // The division of the work. Even: every unit is cut into parts of its own, about as many as its share of
-// the CTAs, and a CTA has one part. Line: the costs of all tiles form one line, cut into ranges of equal
-// length, and a CTA has the tiles that start in its range, of one or several units. The even division is
+// the CTAs, and a CTA has one part. Line: the costs of all units form one line, cut into ranges of equal
+// length, and a CTA has the tiles that start in its range, of one or several units (a unit's own cost lies
+// with its first tile). The even division is
 // taken where its largest part does not exceed the range by more than a switch of units costs.
 // (All costs fit 31 bits, which the host checks with the capacity.)
 struct TreeShare {
@@ -105,7 +110,7 @@ struct TreeShare {
   bool even;
   __device__ int at(int c) const { return min(total, c * each + min(c, more)); }
   __device__ int parts(const TreeSeq& s, int rg) const {
-    const int n = (int)(s.tiles * s.cost(rg) * per_cost), most = (s.tiles + kTreeMinTiles - 1) / kTreeMinTiles;
+    const int n = (int)(s.unit(rg) * per_cost), most = (s.tiles + kTreeMinTiles - 1) / kTreeMinTiles;
     return max(1, min(n, most));
   }
   __device__ int head_parts(const TreeSeq& s) const {
@@ -115,7 +120,7 @@ struct TreeShare {
     int x = 0;
     for (int rg = 0; rg < s.groups; rg += max(1, s.groups - 1)) {
       const int n = parts(s, rg);
-      x = max(x, (s.tiles + n - 1) / n * s.cost(rg));
+      x = max(x, kTreeUnit + (s.tiles + n - 1) / n * s.cost(rg));
     }
     return x;
   }
@@ -152,7 +157,7 @@ struct TreeWalk {
     const int head = d.even ? d.head_parts(s) : s.head();
     kvh = off / head;
     int r = off - kvh * head;
-    const int n = d.even ? d.parts(s, 0) : s.tiles * s.cost(0);  // of a unit, all but the last
+    const int n = d.even ? d.parts(s, 0) : s.unit(0);  // of a unit, all but the last
     rg = min(r / n, s.groups - 1);
     r -= rg * n;
     part = parts = 0;
@@ -165,9 +170,9 @@ struct TreeWalk {
     } else {
       const int w = s.cost(rg);
       left = d.at(c + 1) - d.at(c) + r;
-      t = (r + w - 1) / w;
-      if (t == s.tiles) {
-        left -= s.tiles * w;
+      t = r == 0 ? 0 : max(1, (r - kTreeUnit + w - 1) / w);  // tile t > 0 starts at kTreeUnit + t w
+      if (t >= s.tiles) {
+        left -= s.unit(rg);
         t = 0;
         ++rg;
       }
@@ -185,7 +190,7 @@ struct TreeWalk {
         kvh = 0;
       }
       const int w = s.cost(rg);
-      t1 = min(s.tiles, (left + w - 1) / w);
+      t1 = min(s.tiles, max(1, (left - kTreeUnit + w - 1) / w));
     }
     g.b = b;
     g.kvh = kvh;
@@ -199,7 +204,7 @@ struct TreeWalk {
     g.slot = 2 * c + (first && t > 0 ? 0 : 1);
     first = false;
     if (parts == 0 && t1 == s.tiles) {
-      left -= s.tiles * s.cost(rg);
+      left -= s.unit(rg);
       t = 0;
       ++rg;
     } else {
@@ -221,7 +226,7 @@ __device__ __forceinline__ TreeShare tree_start(const TreeAttnArgs& a, int c, in
     const TreeSeq s = base ? tree_lane_seq(a, base) : first;
     d.total += __reduce_add_sync(0xffffffffu, s.head() * a.Hkv);
   }
-  d.ctas = max(1, min(sms, d.total / kTreeCost2));
+  d.ctas = max(1, min(sms, d.total / (kTreeUnit + kTreeCost2)));  // every range holds a tile's start
   d.each = d.total / d.ctas;
   d.more = d.total - d.each * d.ctas;
   d.per_cost = (float)sms / (float)max(1, d.total);
@@ -381,12 +386,6 @@ __device__ __forceinline__ void tree_store8(const TreeAttnArgs& a, size_t at, co
   for (int i = 0; i < 4; ++i)
     w[i] = a.out_type == ORTHRUS_BF16 ? tree_pack<true>(x[2 * i], x[2 * i + 1]) : tree_pack<false>(x[2 * i], x[2 * i + 1]);
   *reinterpret_cast<uint4*>((uint16_t*)a.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// element offset of a unit's row in out
-__device__ __forceinline__ size_t tree_out_at(const TreeAttnArgs& a, int b, int kvh, int row) {
-  const int node = row / a.G;
-  return (((size_t)b * a.N + node) * a.Hkv * a.G + (size_t)kvh * a.G + (row - node * a.G)) * a.d;
 }
 
 // ---- the kernel -------------------------------------------------------------------------------
@@ -570,11 +569,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int i = 4; i < 60; i += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], v[i + 2 * q], v[i + 2 * q + 1]);
-          const float mt = fmaxf(max3(mx[0], mx[1], fmaxf(v[60], v[61])), max3(mx[2], mx[3], fmaxf(v[62], v[63]))) * sl;
+          const float mt = max3(max3(mx[0], mx[1], v[60]), max3(mx[2], mx[3], v[61]), fmaxf(v[62], v[63])) * sl;
           if (k == k0) {
             m = mt;
           } else {
-            const bool move = mt > m + kTreeSlack;
+            const bool move = row_ok && mt > m + kTreeSlack;
             if (__any_sync(0xffffffffu, move)) {
               // the stream's last product is complete before its sums are scaled
               ok = __all_sync(0xffffffffu, tree_wait(&ms.o_done[st], (cnt - 1) & 1, a.status));
@@ -700,6 +699,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---- loads: K and V in the order of their use, and q when the first K tiles are on their way (they
       // fill free stages while the last segment's scores still read its q) ----
       if (lane == 0 && ok) {
+        const uint64_t once = policy_evict_first();  // K and V are read once; the parts of cut units stay in L2
         const int z = g.b * a.Hkv + g.kvh, lead = min(ahead, nt);
 #pragma unroll 1
         for (int p = 0; p < 2 * nt; ++p) {
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int y = (blk ? t - ct : t) * kTreeKeys;
           uint8_t* dst = ring + s * S::kTile;
 #pragma unroll
-          for (int e = 0; e < kHalves; ++e) tma_load_3d(dst + e * kHalf, map, &ms.full[s], e * 64, y, z);
+          for (int e = 0; e < kHalves; ++e) tma_load_3d_hint(dst + e * kHalf, map, &ms.full[s], e * 64, y, z, once);
         }
       }
     } else if (warp <= kTreeMmaWarp + 1) {
@@ -807,12 +807,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (share.even) {
         last = walk.part == 1 ? c + walk.parts - 2 : -1;
       } else {
-        const int u0 = share.at(c) - skipped, tail = u0 + (g.tiles - 1) * (two ? kTreeCost2 : kTreeCost1);
+        const int u0 = share.at(c) - skipped, tail = u0 + kTreeUnit + (g.tiles - 1) * (two ? kTreeCost2 : kTreeCost1);
         if (share.at(c - 1) > u0) last = -1;
         else
           while (last + 1 < share.ctas && share.at(last + 1) <= tail) ++last;
       }
-      if (last >= 0) note = make_int4(g.b, g.kvh, g.rg, last);
+      if (last >= 0) note = make_int4(g.b, g.kvh, g.rg << 16 | min(kTreeRows, g.live * a.G - g.rg * kTreeRows), last);
     }
     base += 2 * nt;
     ++seg;
@@ -847,103 +847,113 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // ---- joining the parts of a cut unit ---------------------------------------------------------
 
-// CTA x takes the x-th of the notes that name a cut unit, and joins 32 rows x 32 columns of its
-// parts, thread = (row, 4 columns), in key order:
+// CTA x takes the x-th of the notes that name a cut unit, and joins 32 rows of its parts, thread = (row,
+// 4 columns of each of E column groups), in key order:
 //     out = sum_c w_c O_c / sum_c w_c l_c,   w_c = 2^(m_c - max m),
-// eight parts at a time with a running maximum, their loads all in flight together. Bound by the
-// latency of three dependent loads from L2 (notes, parts, and the wait for the first kernel).
+// P parts at a time with a running maximum, all their loads in flight together. Bound by the latency of
+// two dependent loads from L2 (notes, parts) and the wait for the first kernel: E x P = 16 loads a thread.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 8;
 
-__device__ __forceinline__ void tree_join(const TreeAttnArgs& a, const int4& note, int c0, int n, int lrow, int rows,
-                                          int e4) {
+template <int E>
+__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a, int sms) {
+  constexpr int P = 16 / E;
+  __shared__ int before[kJoinThreads / 32];
+  __shared__ int4 found;
+  __shared__ int found_at;
+  const int r = threadIdx.x & 31, part = threadIdx.x >> 5;
+  griddep_wait();
+  griddep_launch();
+  if (threadIdx.x == 0) found_at = -1;
+  int left = blockIdx.x;
+  for (int c = 1; c < sms; c += kJoinThreads) {
+    const int4 note = c + (int)threadIdx.x < sms ? __ldcg(&a.note[c + threadIdx.x]) : make_int4(-1, 0, 0, 0);
+    const unsigned int bal = __ballot_sync(0xffffffffu, note.x >= 0);
+    __syncthreads();
+    if (r == 0) before[part] = __popc(bal);
+    __syncthreads();
+    int at = __popc(bal & ((1u << r) - 1u)), all = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < part) at += before[w];
+      all += before[w];
+    }
+    if (note.x >= 0 && at == left) {
+      found = note;
+      found_at = c + threadIdx.x;
+    }
+    left -= all;
+  }
+  __syncthreads();
+  if (found_at < 0) return;
+  const int4 note = found;
+  const int rg = note.z >> 16, rows = note.z & 0xffff, c0 = found_at - 1, n = note.w - c0 + 1;
+  const int lrow = blockIdx.y * 32 + r;
+  if ((int)blockIdx.y * 32 >= rows) return;
+  const int e4 = blockIdx.z * 8 * E + part;  // and every 8th from there
   const float2* ml = a.part_ml + lrow;
   const float4* po = a.part_o + (size_t)e4 * kTreeRows + lrow;
   float top = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += kJoinParts) {
-    float2 m[kJoinParts];
-    float4 x[kJoinParts];
+  float4 o[E];
 #pragma unroll
-    for (int i = 0; i < kJoinParts; ++i) {
+  for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += P) {
+    float2 m[P];
+    float4 x[P][E];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
       m[i] = make_float2(-INFINITY, 0.f);
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + i < n) {
         // slot of part i: all but the first start inside the unit and use their CTA's first slot
         const size_t slot = (size_t)(2 * (c0 + i0 + i) + (i0 + i == 0 ? 1 : 0));
         m[i] = __ldcg(ml + slot * kTreeRows);
-        x[i] = __ldcg(po + slot * (a.d / 4) * kTreeRows);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i][e] = __ldcg(po + (slot * (a.d / 4) + 8 * e) * kTreeRows);
       }
     }
     float next = top;
 #pragma unroll
-    for (int i = 0; i < kJoinParts; ++i) next = fmaxf(next, m[i].x);
+    for (int i = 0; i < P; ++i) next = fmaxf(next, m[i].x);
     const float ref = next == -INFINITY ? 0.f : next, f = exp2f(top - ref);
-    l *= f;
-    o.x *= f;
-    o.y *= f;
-    o.z *= f;
-    o.w *= f;
     top = next;
+    l *= f;
 #pragma unroll
-    for (int i = 0; i < kJoinParts; ++i) {
+    for (int e = 0; e < E; ++e) o[e] = make_float4(o[e].x * f, o[e].y * f, o[e].z * f, o[e].w * f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
       if (i0 + i < n) {
         const float w = exp2f(m[i].x - ref);
         l += m[i].y * w;
-        o.x += x[i].x * w;
-        o.y += x[i].y * w;
-        o.z += x[i].z * w;
-        o.w += x[i].w * w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          o[e].x += x[i][e].x * w;
+          o[e].y += x[i][e].y * w;
+          o[e].z += x[i][e].z * w;
+          o[e].w += x[i][e].w * w;
+        }
       }
     }
   }
   if (lrow >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const size_t to = tree_out_at(a, note.x, note.y, note.z * kTreeRows + lrow) + e4 * 4;
-  const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  if (a.out_type == ORTHRUS_FP16) {
-    *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(tree_pack<false>(y[0], y[1]), tree_pack<false>(y[2], y[3]));
-  } else if (a.out_type == ORTHRUS_BF16) {
-    *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(tree_pack<true>(y[0], y[1]), tree_pack<true>(y[2], y[3]));
-  } else {
-    uint32_t h0, h1, l0, l1;
-    split_bf16x2(y[0], y[1], h0, l0);
-    split_bf16x2(y[2], y[3], h1, l1);
-    *reinterpret_cast<uint2*>((uint16_t*)a.out + to) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2*>((uint16_t*)a.out + a.out_lo + to) = make_uint2(l0, l1);
-  }
-}
-
-__global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a, int sms) {
-  __shared__ int found, before[kJoinThreads / 32];
-  const int r = threadIdx.x & 31, part = threadIdx.x >> 5;
-  if (threadIdx.x == 0) found = -1;
-  griddep_wait();
-  griddep_launch();
-  const int mine = threadIdx.x + 1;
-  for (int c = mine, left = blockIdx.x; c - (int)threadIdx.x < sms; c += kJoinThreads) {  // one lap for up to 257 CTAs
-    const bool cut = c < sms && __ldcg(&a.note[c]).x >= 0;
-    const unsigned int bal = __ballot_sync(0xffffffffu, cut);
-    __syncthreads();
-    if (r == 0) before[part] = __popc(bal);
-    __syncthreads();
-    int at = __popc(bal & ((1u << r) - 1u)), all = 0;
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-      if (w < part) at += before[w];
-      all += before[w];
+  const int row = rg * kTreeRows + lrow, node = row / a.G;
+  const size_t to = (((size_t)note.x * a.N + node) * a.Hkv * a.G + (size_t)note.y * a.G + (row - node * a.G)) * a.d + e4 * 4;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float y[4] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv};
+    uint2* dst = reinterpret_cast<uint2*>((uint16_t*)a.out + to + 32 * e);
+    if (a.out_type == ORTHRUS_FP16) {
+      *dst = make_uint2(tree_pack<false>(y[0], y[1]), tree_pack<false>(y[2], y[3]));
+    } else if (a.out_type == ORTHRUS_BF16) {
+      *dst = make_uint2(tree_pack<true>(y[0], y[1]), tree_pack<true>(y[2], y[3]));
+    } else {
+      uint32_t h0, h1, l0, l1;
+      split_bf16x2(y[0], y[1], h0, l0);
+      split_bf16x2(y[2], y[3], h1, l1);
+      *dst = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>((uint16_t*)a.out + a.out_lo + to + 32 * e) = make_uint2(l0, l1);
     }
-    if (cut && at == left) found = c;
-    left -= all;
   }
-  __syncthreads();
-  if (found < 0) return;
-  const int4 note = __ldcg(&a.note[found]);
-  const int lrow = blockIdx.y * 32 + r;
-  const int live = a.n_nodes ? min(max(a.n_nodes[note.x], 0), a.N) : a.N;
-  const int rows = live * a.G - note.z * kTreeRows;
-  if ((int)blockIdx.y * 32 >= rows) return;
-  const int c0 = found - 1, n = note.w - c0 + 1;
-  for (int e4 = blockIdx.z * 8 + part; e4 < a.d / 4; e4 += 8 * gridDim.z) tree_join(a, note, c0, n, lrow, rows, e4);
 }
 
 }  // namespace orthrus
