@@ -261,8 +261,8 @@ def linear_workspace_bytes(M, N, Kd) -> int:
 _TYPES = {torch.float32: FP32, torch.bfloat16: BF16, torch.float16: FP16}
 
 
-_PART = struct.Struct("PPiiiiiiqqqqqqq")  # orthrus_rotary_part
-assert _PART.size == C.sizeof(RotaryPart)
+_PARTS = [struct.Struct("PPiiiiiiqqqqqqq" * n) for n in range(ROTARY_MAX_PARTS + 1)]  # orthrus_rotary_part [n]
+assert _PARTS[3].size == 3 * C.sizeof(RotaryPart)
 
 
 def _on(dev, stream):
@@ -290,41 +290,42 @@ def _arg(ok, call, what):
         raise ValueError(f"{call}: {what}")
 
 
-def _dense(call, dev, dtype, shape, names, *tensors):
-    """Every given tensor lies densely on device `dev`, with this dtype and shape (None: any)."""
-    for i, t in enumerate(tensors):
-        if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-                and (shape is None or t.shape == shape)):
-            raise ValueError(f"{call}: {names.split()[i]} must be a contiguous {dtype} tensor on device {dev}"
+def _refuse(call, dev, wanted):
+    """Raise for the first tensor of `wanted` (name, tensor, dtype, shape) that is not densely on device `dev` with
+    that dtype and shape. Called when the one-expression check of a call has failed."""
+    for name, t, dtype, shape in wanted:
+        if t is None or not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+                             and (shape is None or tuple(t.shape) == tuple(shape))):
+            raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor on device {dev}"
                              + ("" if shape is None else f" of shape {tuple(shape)}"))
+    raise ValueError(f"{call}: the tensors do not fit one another")
 
 
-def _batch_ints(call, dev, B, names, *tensors):
-    """int32 [batch] arrays, None where they are optional; their addresses."""
-    out = []
-    for i, t in enumerate(tensors):
-        if t is None:
-            out.append(None)
-            continue
-        if not (t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous() and t.numel() == B):
-            raise ValueError(f"{call}: {names.split()[i]} must be int32 [{B}] on device {dev}")
-        out.append(t.data_ptr())
-    return out
+_I = torch.int32
+
+
+def _optional(call, dev, n, name, t):
+    """Address of an optional int32 array of n elements."""
+    if t is None:
+        return None
+    if not (t.dtype is _I and t.get_device() == dev and t.numel() == n and t.is_contiguous()):
+        _refuse(call, dev, [(name, t, _I, (n,))])
+    return t.data_ptr()
 
 
 def tree_layout(parents, depth, mask, n_nodes=None, status=None, stream=None):
     """Depths and visibility words of draft trees. parents: int32 [B][N]; depth: int32 [B][N]; mask:
     int64 [B][N][ceil(N / 64)] (the words' bits)."""
-    dev, name = parents.get_device(), "tree_layout"
-    shape = parents.shape
+    dev, name, shape = parents.get_device(), "tree_layout", parents.shape
     _arg(dev >= 0 and _length(shape) == 2, name, "parents must be [batch][nodes] on a GPU")
     B, N = shape
-    _dense(name, dev, torch.int32, shape, "parents depth", parents, depth)
-    _dense(name, dev, torch.int64, (B, N, (N + 63) // 64), "mask", mask)
-    nn, = _batch_ints(name, dev, B, "n_nodes", n_nodes)
-    st, = _batch_ints(name, dev, 1, "status", status)
-    _call(dev, load().orthrus_tree_layout, parents.data_ptr(), nn, B, N, depth.data_ptr(), mask.data_ptr(), st,
-          _on(dev, stream))
+    words = (B, N, (N + 63) // 64)
+    if not (parents.dtype is _I and parents.is_contiguous() and depth.dtype is _I and depth.get_device() == dev
+            and depth.is_contiguous() and depth.shape == shape and mask.dtype is torch.int64
+            and mask.get_device() == dev and mask.is_contiguous() and mask.shape == words):
+        _refuse(name, dev, [("parents", parents, _I, None), ("depth", depth, _I, shape), ("mask", mask, torch.int64, words)])
+    _call(dev, load().orthrus_tree_layout, parents.data_ptr(), _optional(name, dev, B, "n_nodes", n_nodes), B, N,
+          depth.data_ptr(), mask.data_ptr(), _optional(name, dev, 1, "status", status), _on(dev, stream))
 
 
 def tree_attention_workspace_bytes(batch, n_kv_heads, group, nodes, head_dim) -> int:
@@ -346,22 +347,25 @@ def tree_attention(q, k_cache, v_cache, k_blk, v_blk, len, mask, out, workspace,
     G = R // N
     _arg(G * N == R, name, "mask does not fit q")
     _arg(k_cache.dim() == 4 and k_blk.dim() == 4 and k_blk.size(2) >= N, name, "a cache or block has another shape")
-    cap, rows = k_cache.size(2), k_blk.size(2)
-    _dense(name, dev, t, None, "q", q)
-    _dense(name, dev, t, (B, H, cap, d), "k_cache v_cache", k_cache, v_cache)
-    _dense(name, dev, t, (B, H, rows, d), "k_blk v_blk", k_blk, v_blk)
-    _dense(name, dev, torch.int64, (B, N, (N + 63) // 64), "mask", mask)
-    _arg(len is not None, name, "len must be given")
-    ln, nn = _batch_ints(name, dev, B, "len n_nodes", len, n_nodes)
-    st, = _batch_ints(name, dev, 1, "status", status)
+    cap, rows, words = k_cache.size(2), k_blk.size(2), (B, N, (N + 63) // 64)
+    cs, bs = (B, H, cap, d), (B, H, rows, d)
     planes, to = out.dim() == 3, out.dtype
+    os_ = (2, B * N, H * G * d) if planes else (B * N, H * G * d)
     _arg(to is torch.bfloat16 or (to is torch.float16 and not planes), name, "out must be fp16 or bf16, planes bf16")
-    _dense(name, dev, to, (2, B * N, H * G * d) if planes else (B * N, H * G * d), "out", out)
-    _dense(name, dev, workspace.dtype, None, "workspace", workspace)
+    if not (q.is_contiguous() and k_cache.dtype is t and k_cache.get_device() == dev and k_cache.is_contiguous()
+            and k_cache.shape == cs and v_cache.dtype is t and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and v_cache.shape == cs and k_blk.dtype is t and k_blk.get_device() == dev and k_blk.is_contiguous()
+            and k_blk.shape == bs and v_blk.dtype is t and v_blk.get_device() == dev and v_blk.is_contiguous()
+            and v_blk.shape == bs and mask.dtype is torch.int64 and mask.get_device() == dev and mask.is_contiguous()
+            and mask.shape == words and out.get_device() == dev and out.is_contiguous() and out.shape == os_
+            and len is not None and workspace.get_device() == dev and workspace.is_contiguous()):
+        _refuse(name, dev, [("q", q, t, None), ("k_cache", k_cache, t, cs), ("v_cache", v_cache, t, cs), ("k_blk", k_blk, t, bs),
+                            ("v_blk", v_blk, t, bs), ("mask", mask, torch.int64, words), ("out", out, to, os_),
+                            ("len", len, _I, (B,)), ("workspace", workspace, workspace.dtype, None)])
     _call(dev, load().orthrus_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_blk.data_ptr(),
-          v_blk.data_ptr(), ln, nn, mask.data_ptr(), B, H, G, N, d, cap, rows, _TYPES[t],
-          BF16_PLANES if planes else _TYPES[to], scale, out.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), st, _on(dev, stream))
+          v_blk.data_ptr(), _optional(name, dev, B, "len", len), _optional(name, dev, B, "n_nodes", n_nodes), mask.data_ptr(),
+          B, H, G, N, d, cap, rows, _TYPES[t], BF16_PLANES if planes else _TYPES[to], scale, out.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes, _optional(name, dev, 1, "status", status), _on(dev, stream))
 
 
 def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, new_len, pending, accept_len, path,
@@ -369,27 +373,36 @@ def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, ne
     """Greedy consensus on draft trees and the accepted paths' K/V rows into the cache. k_blk, v_blk:
     [L][B][Hkv][>= N][d] and k_cache, v_cache: [L][B][Hkv][capacity][d] of one 16-bit type; the others int32, [B] or
     [B][N]. new_len may be len."""
-    dev, name = parents.get_device(), "tree_commit"
-    shape = parents.shape
-    _arg(dev >= 0 and _length(shape) == 2, name, "parents must be [batch][nodes] on a GPU")
+    dev, name, shape = parents.get_device(), "tree_commit", parents.shape
+    _arg(dev >= 0 and _length(shape) == 2 and k_cache.dim() == 5 and k_blk.dim() == 5, name,
+         "parents must be [batch][nodes] on a GPU, caches and blocks five-dimensional")
     B, N = shape
-    _dense(name, dev, torch.int32, shape, "parents tokens argmax path committed", parents, tokens, argmax, path, committed)
-    for x in (len, new_len, pending, accept_len):
-        _arg(x is not None, name, "len, new_len, pending and accept_len must be given")
-    ln, nl, pend, acc, nn = _batch_ints(name, dev, B, "len new_len pending accept_len n_nodes", len, new_len, pending,
-                                        accept_len, n_nodes)
-    st, = _batch_ints(name, dev, 1, "status", status)
     t = k_cache.dtype
-    _arg(k_cache.dim() == 5 and k_blk.dim() == 5 and t.itemsize == 2, name,
-         "caches and blocks must be five-dimensional with 16-bit elements")
     L, _, H, cap, d = k_cache.shape
     rows = k_blk.size(3)
-    _arg(rows >= N, name, "k_blk and v_blk must hold a row for every node")
-    _dense(name, dev, t, (L, B, H, cap, d), "k_cache v_cache", k_cache, v_cache)
-    _dense(name, dev, t, (L, B, H, rows, d), "k_blk v_blk", k_blk, v_blk)
-    _call(dev, load().orthrus_tree_commit, parents.data_ptr(), tokens.data_ptr(), argmax.data_ptr(), nn, k_blk.data_ptr(),
-          v_blk.data_ptr(), rows, k_cache.data_ptr(), v_cache.data_ptr(), L, B, H, cap, d, N, ln, nl, pend, acc,
-          path.data_ptr(), committed.data_ptr(), st, _on(dev, stream))
+    cs, bs = (L, B, H, cap, d), (L, B, H, rows, d)
+    if not (t.itemsize == 2 and rows >= N and parents.dtype is _I and parents.is_contiguous()
+            and tokens.dtype is _I and tokens.get_device() == dev and tokens.is_contiguous() and tokens.shape == shape
+            and argmax.dtype is _I and argmax.get_device() == dev and argmax.is_contiguous() and argmax.shape == shape
+            and path.dtype is _I and path.get_device() == dev and path.is_contiguous() and path.shape == shape
+            and committed.dtype is _I and committed.get_device() == dev and committed.is_contiguous()
+            and committed.shape == shape and k_cache.get_device() == dev and k_cache.is_contiguous()
+            and k_cache.shape == cs and v_cache.dtype is t and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and v_cache.shape == cs and k_blk.dtype is t and k_blk.get_device() == dev and k_blk.is_contiguous()
+            and k_blk.shape == bs and v_blk.dtype is t and v_blk.get_device() == dev and v_blk.is_contiguous()
+            and v_blk.shape == bs and len is not None and new_len is not None and pending is not None
+            and accept_len is not None):
+        _refuse(name, dev, [("parents", parents, _I, None), ("tokens", tokens, _I, shape), ("argmax", argmax, _I, shape),
+                            ("path", path, _I, shape), ("committed", committed, _I, shape), ("k_cache", k_cache, t, cs),
+                            ("v_cache", v_cache, t, cs), ("k_blk", k_blk, t, bs), ("v_blk", v_blk, t, bs),
+                            ("len", len, _I, (B,)), ("new_len", new_len, _I, (B,)), ("pending", pending, _I, (B,)),
+                            ("accept_len", accept_len, _I, (B,))])
+    _call(dev, load().orthrus_tree_commit, parents.data_ptr(), tokens.data_ptr(), argmax.data_ptr(),
+          _optional(name, dev, B, "n_nodes", n_nodes), k_blk.data_ptr(), v_blk.data_ptr(), rows, k_cache.data_ptr(),
+          v_cache.data_ptr(), L, B, H, cap, d, N, _optional(name, dev, B, "len", len),
+          _optional(name, dev, B, "new_len", new_len), _optional(name, dev, B, "pending", pending),
+          _optional(name, dev, B, "accept_len", accept_len), path.data_ptr(), committed.data_ptr(),
+          _optional(name, dev, 1, "status", status), _on(dev, stream))
 
 
 @functools.lru_cache(maxsize=64)
@@ -418,27 +431,36 @@ def rotary(rope, parts, len=None, offsets=None, inverse=False, status=None, stre
     dev = first.get_device()
     _arg(dev >= 0 and first.dim() == 4, name, "src must be [batch][tokens][heads][d] on a GPU")
     B, T = first.size(0), first.size(1)
-    packed = b""
-    for src, dst, *flags in parts:
-        flags = flags[0] if flags else 0
+    values = []
+    for part in parts:
+        src, dst = part[0], part[1]
+        flags = part[2] if _length(part) > 2 else 0
         ss, ds, sh, dh = src.stride(), dst.stride(), src.shape, dst.shape
-        _arg(src.get_device() == dev and dst.get_device() == dev and src.dtype in _TYPES and dst.dtype in _TYPES, name,
-             "tensors must be fp32, bf16 or fp16 on one GPU")
-        _arg(_length(sh) == 4 and sh[0] == B and sh[1] == T and sh[3] == hd and (ss[3] == 1), name,
-             "src must be [batch][tokens][heads][d] with a dense last dimension")
-        heads, nd = sh[2], _length(dh)
-        group = dh[3] if nd == 5 else 1
-        _arg((nd == 4 or nd == 5) and dh[0] == B and dh[-1] == hd and ds[-1] == 1 and dh[2] * group == heads
-             and (flags & ROTARY_APPEND or dh[1] == T), name,
-             "dst must be [batch][rows][heads][d] or [batch][rows][kv heads][group][d] with a dense last dimension")
-        packed += _PART.pack(src.data_ptr(), dst.data_ptr(), _TYPES[src.dtype], _TYPES[dst.dtype], heads, group, flags,
-                             dh[1], ss[0], ss[1], ss[2], ds[0], ds[1], ds[2], ds[3] if nd == 5 else 0)
-    ln, = _batch_ints(name, dev, B, "len", len)
-    st, = _batch_ints(name, dev, 1, "status", status)
+        a, b, nd = _TYPES.get(src.dtype), _TYPES.get(dst.dtype), _length(dh)
+        if not (a is not None and b is not None and src.get_device() == dev and dst.get_device() == dev):
+            raise ValueError("rotary: tensors must be fp32, bf16 or fp16 on one GPU")
+        if not (_length(sh) == 4 and sh[0] == B and sh[1] == T and sh[3] == hd and ss[3] == 1):
+            raise ValueError("rotary: src must be [batch][tokens][heads][d] with a dense last dimension")
+        if nd == 4:
+            group, heads, inner = 1, dh[2], 0
+        elif nd == 5:
+            group, heads, inner = dh[3], dh[2] * dh[3], ds[3]
+        else:
+            group = heads = inner = 0
+        if not (heads == sh[2] and dh[0] == B and dh[-1] == hd and ds[-1] == 1 and (flags & ROTARY_APPEND or dh[1] == T)):
+            raise ValueError("rotary: dst must be [batch][rows][heads][d] or [batch][rows][kv heads][group][d] with a "
+                             "dense last dimension")
+        values += (src.data_ptr(), dst.data_ptr(), a, b, heads, group, flags, dh[1], ss[0], ss[1], ss[2], ds[0], ds[1],
+                   ds[2], inner)
+    off = None
     if offsets is not None:
-        _dense(name, dev, torch.int32, (B, T), "offsets", offsets)
-    _call(dev, load().orthrus_rotary, C.addressof(rope), packed, n, B, T, ln, None if offsets is None else offsets.data_ptr(),
-          1 if inverse else 0, st, _on(dev, stream))
+        if not (offsets.dtype is _I and offsets.get_device() == dev and offsets.is_contiguous()
+                and offsets.shape == (B, T)):
+            _refuse(name, dev, [("offsets", offsets, _I, (B, T))])
+        off = offsets.data_ptr()
+    _call(dev, load().orthrus_rotary, C.addressof(rope), _PARTS[n].pack(*values), n, B, T,
+          _optional(name, dev, B, "len", len), off, 1 if inverse else 0, _optional(name, dev, 1, "status", status),
+          _on(dev, stream))
 
 
 # ---- a plan with its device buffers --------------------------------------------------------------
