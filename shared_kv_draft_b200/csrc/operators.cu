@@ -276,6 +276,7 @@ orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_par
     a.part[i] = p;
   }
   if (batch == 0 || tokens == 0) return ORTHRUS_OK;
+  if ((long long)batch * tokens > INT32_MAX) return ORTHRUS_ERR_ARG;
   a.n_parts = n_parts;
   a.head_dim = rope->head_dim;
   a.rot_dim = rope->rot_dim;
@@ -284,24 +285,35 @@ orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_par
   a.gain = rope->gain;
   a.batch = batch;
   a.tokens = tokens;
-  a.vec = vec;
-  a.total_items = 0;
-  const int per_head = rope->head_dim / (vec ? 16 : 2);
+  a.heads = 0;
   for (int i = 0; i < n_parts; ++i) {
-    a.items[i] = parts[i].heads * per_head;
-    a.total_items += a.items[i];
+    a.heads += parts[i].heads;
+    a.per_group[i] = (uint32_t)(((1ull << 32) + parts[i].group - 1) / parts[i].group);
   }
+  a.per_heads = (uint32_t)(((1ull << 32) + a.heads - 1) / a.heads);
+  a.units = rope->head_dim / (vec ? 16 : 2);
+  a.slots = kRotaryThreads / a.units;
   a.len = len;
   a.offsets = offsets;
   a.status = status;
+  // many tokens: several to a CTA, whose angles are then a small part of its work; few: a CTA each, and
+  // their heads over up to eight
   const long long all = (long long)batch * tokens;
-  a.tok_per_cta = all >= 8 * num_sms() ? kRotaryTokens : 1;
+  a.tok_per_cta = (int)std::min<long long>(kRotaryTokens, std::max(1ll, all / (8 * num_sms())));
   const long long gx = (all + a.tok_per_cta - 1) / a.tok_per_cta;
-  if (gx > INT32_MAX) return ORTHRUS_ERR_ARG;
-  // few tokens: their heads are spread over up to eight CTAs
   int gy = 1;
-  while (gy < 8 && gx * gy < num_sms() && gy * kRotaryThreads < a.total_items) gy *= 2;
-  return launch(rotary_kernel, dim3((unsigned)gx, gy), dim3(kRotaryThreads), 0, (cudaStream_t)stream, a) == cudaSuccess
+  while (gy < 8 && gx * gy < num_sms() && gy * a.slots < a.heads) gy *= 2;
+  // one pair of types for all parts in the usual cases
+  bool same = vec;
+  for (int i = 1; i < n_parts; ++i)
+    same = same && parts[i].src_type == parts[0].src_type && parts[i].dst_type == parts[0].dst_type;
+  const int from = parts[0].src_type, to = parts[0].dst_type;
+  void (*kernel)(RotaryArgs) = vec ? rotary_kernel<8, kAnyType, kAnyType> : rotary_kernel<1, kAnyType, kAnyType>;
+  if (same && from == ORTHRUS_FP32 && to == ORTHRUS_FP16) kernel = rotary_kernel<8, ORTHRUS_FP32, ORTHRUS_FP16>;
+  if (same && from == ORTHRUS_FP32 && to == ORTHRUS_FP32) kernel = rotary_kernel<8, ORTHRUS_FP32, ORTHRUS_FP32>;
+  if (same && from == ORTHRUS_BF16 && to == ORTHRUS_BF16) kernel = rotary_kernel<8, ORTHRUS_BF16, ORTHRUS_BF16>;
+  if (same && from == ORTHRUS_FP16 && to == ORTHRUS_FP16) kernel = rotary_kernel<8, ORTHRUS_FP16, ORTHRUS_FP16>;
+  return launch(kernel, dim3((unsigned)gx, gy), dim3(kRotaryThreads), 0, (cudaStream_t)stream, a) == cudaSuccess
              ? ORTHRUS_OK
              : ORTHRUS_ERR_CUDA;
 }

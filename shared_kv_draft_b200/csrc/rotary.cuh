@@ -11,30 +11,36 @@
 // the rest, in [-1/2, 1/2] turns, goes through CUDA's sincospif in fp32: the angle is then
 // off by about 2^-25 turns, like one fp32 rounding.
 #pragma once
+#include <limits.h>
+
 #include "ptx.cuh"
 
 namespace orthrus {
 
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryMaxPairs = 128;
-constexpr int kRotaryTokens = 4;  // tokens of one CTA at most
+constexpr int kRotaryTokens = 8;  // tokens of one CTA at most
+constexpr int kAnyType = -1;      // types of the parts at run time
 
 struct RotaryArgs {
   double turns[kRotaryMaxPairs];
   orthrus_rotary_part part[ORTHRUS_ROTARY_MAX_PARTS];
+  uint32_t per_group[ORTHRUS_ROTARY_MAX_PARTS];  // ceil(2^32 / group): h / group = its high product with h < 2^16
   int n_parts, head_dim, rot_dim, interleaved, inverse;
   float gain;
-  int batch, tokens, tok_per_cta, vec;
-  int items[ORTHRUS_ROTARY_MAX_PARTS];  // units of work of one token: heads x units of a head
-  int total_items;
+  int batch, tokens, tok_per_cta;
+  int heads;               // of all parts
+  uint32_t per_heads;      // ceil(2^32 / heads)
+  int units, slots;        // units of a head, heads that a CTA has in hand at a time
   const int* len;
   const int* offsets;
   int* status;
 };
 
-// n values from / to memory of a run-time type; n is 1, or 8 at 16-byte aligned addresses
-template <int N>
-__device__ __forceinline__ void rot_load(const void* p, size_t at, int type, float* x) {
+// N values from / to memory of type T, or `type` where T is kAnyType; N is 1, or 8 at 16-byte aligned addresses
+template <int N, int T>
+__device__ __forceinline__ void rot_load(const void* p, long long at, int type, float* x) {
+  if (T != kAnyType) type = T;
   if constexpr (N == 8) {
     if (type == ORTHRUS_FP32) {
       const float4* q = reinterpret_cast<const float4*>((const float*)p + at);
@@ -60,8 +66,9 @@ __device__ __forceinline__ void rot_load(const void* p, size_t at, int type, flo
   }
 }
 
-template <int N>
-__device__ __forceinline__ void rot_store(void* p, size_t at, int type, bool bf16_values, float* x) {
+template <int N, int T>
+__device__ __forceinline__ void rot_store(void* p, long long at, int type, bool bf16_values, float* x) {
+  if (T != kAnyType) type = T;
   if (bf16_values) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = kv_value(x[i]);
@@ -92,101 +99,86 @@ __device__ __forceinline__ void rot_store(void* p, size_t at, int type, bool bf1
   }
 }
 
-// One unit of a head: N pairs (2 N values), or 2 N values of the copied tail.
-template <int N>
-__device__ __forceinline__ void rotary_unit(const RotaryArgs& a, const orthrus_rotary_part& p, const float2* cs,
-                                            size_t src, size_t dst, int unit) {
-  const int pairs = a.rot_dim >> 1;
-  const bool bfv = (p.flags & ORTHRUS_ROTARY_BF16_VALUES) != 0;
-  const bool turn = !(p.flags & ORTHRUS_ROTARY_COPY) && unit * N < pairs;
-  int e1, e2;
-  if (turn && !a.interleaved) {
-    e1 = unit * N;
-    e2 = e1 + pairs;
-  } else {
-    e1 = 2 * unit * N;
-    e2 = e1 + N;
-  }
-  float x[N], y[N];
-  rot_load<N>(p.src, src + e1, p.src_type, x);
-  rot_load<N>(p.src, src + e2, p.src_type, y);
-  if (turn) {
-    if (a.interleaved) {
-      // the 2 N values are N neighbouring pairs
-      float z[2 * N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        z[i] = x[i];
-        z[N + i] = y[i];
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 c = cs[unit * N + i];
-        const float u = z[2 * i], v = z[2 * i + 1];
-        z[2 * i] = u * c.x - v * c.y;
-        z[2 * i + 1] = v * c.x + u * c.y;
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i] = z[i];
-        y[i] = z[N + i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 c = cs[unit * N + i];
-        const float u = x[i], v = y[i];
-        x[i] = u * c.x - v * c.y;
-        y[i] = v * c.x + u * c.y;
-      }
-    }
-  }
-  rot_store<N>(p.dst, dst + e1, p.dst_type, bfv, x);
-  rot_store<N>(p.dst, dst + e2, p.dst_type, bfv, y);
-}
-
+// A unit is N pairs of a head (2 N values), or 2 N values of its copied tail; N = 8, or 1 where the sizes, strides
+// or addresses do not allow 16-byte accesses. A thread keeps its unit and goes through the heads of the CTA's
+// tokens. Bound by memory: every value is read and written once. The angles of a token are computed once for all
+// of its heads, and lie in shared memory so that the threads of a warp read consecutive 16 bytes.
+template <int N, int SRC, int DST>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   __shared__ float2 cs[kRotaryTokens * kRotaryMaxPairs];
+  __shared__ long long from[kRotaryTokens][ORTHRUS_ROTARY_MAX_PARTS], to[kRotaryTokens][ORTHRUS_ROTARY_MAX_PARTS];
   griddep_wait();
   griddep_launch();
-  const int pairs = a.rot_dim >> 1;
-  const long long all = (long long)a.batch * a.tokens;
-  const long long t0 = (long long)blockIdx.x * a.tok_per_cta;
-  const int nt = (int)min((long long)a.tok_per_cta, all - t0);
+  const int pairs = a.rot_dim >> 1, rot_units = pairs / N;
+  const int t0 = blockIdx.x * a.tok_per_cta, nt = min(a.tok_per_cta, a.batch * a.tokens - t0);
+  // pair p = unit u's i-th: N = 8 keeps two neighbouring pairs (16 bytes) of all units together
+  auto place = [&](int p) { return N == 1 ? p : ((p & 7) >> 1) * (2 * rot_units) + (p >> 3) * 2 + (p & 1); };
+#pragma unroll 1
   for (int i = threadIdx.x; i < nt * pairs; i += kRotaryThreads) {
     const int k = i / pairs, p = i - k * pairs;
-    const long long m = t0 + k;
-    const int b = (int)(m / a.tokens), t = (int)(m - (long long)b * a.tokens);
+    const int m = t0 + k, b = m / a.tokens, t = m - b * a.tokens;
     const double pos = (double)(a.len ? a.len[b] : 0) + (double)(a.offsets ? a.offsets[m] : t);
     const double turns = pos * a.turns[p];
     const float r = (float)(turns - rint(turns));
     float s, c;
     sincospif(2.f * r, &s, &c);
-    cs[i] = make_float2(c * a.gain, (a.inverse ? -s : s) * a.gain);
+    cs[k * pairs + place(p)] = make_float2(c * a.gain, (a.inverse ? -s : s) * a.gain);
   }
-  __syncthreads();
-  const int per_head = a.vec ? a.head_dim / 16 : a.head_dim / 2;
-  for (int i = blockIdx.y * kRotaryThreads + threadIdx.x; i < nt * a.total_items; i += gridDim.y * kRotaryThreads) {
-    const int k = i / a.total_items;
-    int item = i - k * a.total_items, j = 0;
-    while (j + 1 < a.n_parts && item >= a.items[j]) item -= a.items[j++];
+  if (threadIdx.x < nt * a.n_parts) {
+    const int k = threadIdx.x / a.n_parts, j = threadIdx.x - k * a.n_parts;
     const orthrus_rotary_part& p = a.part[j];
-    const long long m = t0 + k;
-    const int b = (int)(m / a.tokens), t = (int)(m - (long long)b * a.tokens);
-    const int h = item / per_head, unit = item - h * per_head;
+    const int m = t0 + k, b = m / a.tokens, t = m - b * a.tokens;
     long long row = t;
+    bool ok = true;
     if (p.flags & ORTHRUS_ROTARY_APPEND) {
       row += a.len ? a.len[b] : 0;
-      if (row < 0 || row >= p.rows) {
-        if (unit == 0) set_status(a.status, ORTHRUS_ERR_CAPACITY);
-        continue;
+      ok = row >= 0 && row < p.rows;
+      if (!ok) set_status(a.status, ORTHRUS_ERR_CAPACITY);
+    }
+    from[k][j] = ok ? b * p.src_batch + t * p.src_token : LLONG_MIN;  // no such row: nothing is written
+    to[k][j] = b * p.dst_batch + row * p.dst_token;
+  }
+  __syncthreads();
+  const int slot = threadIdx.x / a.units, unit = threadIdx.x - slot * a.units;
+  if (slot >= a.slots) return;
+#pragma unroll 2
+  for (int i = blockIdx.y * a.slots + slot; i < nt * a.heads; i += gridDim.y * a.slots) {
+    const int k = (int)__umulhi((uint32_t)i, a.per_heads);
+    int h = i - k * a.heads, j = 0;
+    while (h >= a.part[j].heads) h -= a.part[j++].heads;
+    const orthrus_rotary_part& p = a.part[j];
+    if (from[k][j] == LLONG_MIN) continue;
+    const int kv = p.group == 1 ? h : (int)__umulhi((uint32_t)h, a.per_group[j]);
+    const long long src = from[k][j] + h * p.src_head;
+    const long long dst = to[k][j] + kv * p.dst_kv + (h - kv * p.group) * p.dst_head;
+    const bool bfv = (p.flags & ORTHRUS_ROTARY_BF16_VALUES) != 0;
+    const bool turn = !(p.flags & ORTHRUS_ROTARY_COPY) && unit < rot_units;
+    const int e1 = turn && !a.interleaved ? unit * N : 2 * unit * N, e2 = e1 + (turn && !a.interleaved ? pairs : N);
+    float x[2 * N];
+    rot_load<N, SRC>(p.src, src + e1, p.src_type, x);
+    rot_load<N, SRC>(p.src, src + e2, p.src_type, x + N);
+    if (turn) {
+      const float2* c = cs + k * pairs;
+      if (a.interleaved) {
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const float2 f = N == 1 ? c[unit] : c[(q >> 1) * (2 * rot_units) + unit * 2 + (q & 1)];
+          const float u = x[2 * q], v = x[2 * q + 1];
+          x[2 * q] = u * f.x - v * f.y;
+          x[2 * q + 1] = v * f.x + u * f.y;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const float2 f = N == 1 ? c[unit] : c[(q >> 1) * (2 * rot_units) + unit * 2 + (q & 1)];
+          const float u = x[q], v = x[N + q];
+          x[q] = u * f.x - v * f.y;
+          x[N + q] = v * f.x + u * f.y;
+        }
       }
     }
-    const size_t src = (size_t)(b * p.src_batch + t * p.src_token + h * p.src_head);
-    const int kv = h / p.group;
-    const size_t dst = (size_t)(b * p.dst_batch + row * p.dst_token + kv * p.dst_kv + (h - kv * p.group) * p.dst_head);
-    if (a.vec) rotary_unit<8>(a, p, cs + k * pairs, src, dst, unit);
-    else rotary_unit<1>(a, p, cs + k * pairs, src, dst, unit);
+    rot_store<N, DST>(p.dst, dst + e1, p.dst_type, bfv, x);
+    rot_store<N, DST>(p.dst, dst + e2, p.dst_type, bfv, x + N);
   }
 }
 
