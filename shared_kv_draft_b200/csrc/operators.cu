@@ -89,11 +89,16 @@ orthrus_status launch_tree_commit(const TreeWalkArgs& w, TreeMoveArgs m, int n_l
   m.batch = w.batch;
   m.nodes = w.nodes;
   m.capacity = w.capacity;
+  m.layers = n_layers;
   m.pieces = head_dim / 8;
   const int warps = std::min(kWalkThreads / 32, w.batch);
-  if (launch(tree_walk_kernel, dim3(1), dim3(32 * warps), 0, st, w) != cudaSuccess) return ORTHRUS_ERR_CUDA;
-  if (launch(tree_move_kernel, dim3((unsigned)((size_t)n_layers * m.batch * m.kv_heads)), dim3(kMoveThreads), 0, st,
-             m) != cudaSuccess)
+  void (*walk)(TreeWalkArgs) = w.nodes <= 64 ? tree_walk_kernel<2> : tree_walk_kernel<kTreeMaxNodes / 32>;
+  if (launch(walk, dim3(1), dim3(32 * warps), 0, st, w) != cudaSuccess) return ORTHRUS_ERR_CUDA;
+  // (layer, head) pairs to a CTA: one while the SMs are not full, then more, for longer streams of loads
+  const long long pairs = (long long)n_layers * m.kv_heads;
+  m.zs = (int)std::min<long long>(8, std::max(1ll, pairs * m.batch / (8 * num_sms())));
+  if (launch(tree_move_kernel, dim3((unsigned)((pairs + m.zs - 1) / m.zs), m.batch), dim3(kMoveThreads), 0, st, m) !=
+      cudaSuccess)
     return ORTHRUS_ERR_CUDA;
   return ORTHRUS_OK;
 }

@@ -88,8 +88,10 @@ __global__ void tree_embed_kernel(const TreeEmbedArgs a) {
 
 // Greedy walk, one warp per sequence: from node 0 to the lowest-indexed child whose token is
 // the argmax at the current node, until there is none. A child has a higher index than its
-// parent, so the walk ends whatever the parents hold. One CTA serves every sequence, so that
-// all of them see the status word as it was before the call.
+// parent, so the walk ends whatever the parents hold. The tree lies in registers, 32 nodes a
+// register, loaded at once; a step is a comparison, a minimum over the warp and a shuffle. One CTA
+// serves every sequence, so that all of them see the status word as it was before the call. Bound
+// by latency: one round of loads, then about 50 cycles a step.
 struct TreeWalkArgs {
   const int *parents, *tokens, *argmax, *n_nodes;
   int batch, nodes, capacity;
@@ -99,6 +101,8 @@ struct TreeWalkArgs {
 
 constexpr int kWalkThreads = 1024;
 
+// R: registers a lane holds of each array, at least nodes / 32
+template <int R>
 __global__ void __launch_bounds__(kWalkThreads) tree_walk_kernel(const TreeWalkArgs a) {
   griddep_wait();
   griddep_launch();
@@ -107,6 +111,14 @@ __global__ void __launch_bounds__(kWalkThreads) tree_walk_kernel(const TreeWalkA
   __syncthreads();
   for (int b = threadIdx.x >> 5; b < a.batch; b += blockDim.x >> 5) {
     const size_t base = (size_t)b * a.nodes;
+    int par[R], tok[R], arg[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int i = k * 32 + lane;
+      par[k] = i < a.nodes ? a.parents[base + i] : -1;
+      tok[k] = i < a.nodes ? a.tokens[base + i] : 0;
+      arg[k] = i < a.nodes ? a.argmax[base + i] : 0;
+    }
     const int old = a.len[b];
     int n = a.n_nodes ? a.n_nodes[b] : a.nodes;
     bool ok = !failed && n > 0;
@@ -115,81 +127,81 @@ __global__ void __launch_bounds__(kWalkThreads) tree_walk_kernel(const TreeWalkA
       ok = false;
     }
     if (!ok) n = 0;
-    int par[kTreeMaxNodes / 32], tok[kTreeMaxNodes / 32];
+    // lane l keeps entries l, l + 32, .. of the path and of the committed tokens
+    int path[R], com[R], cur = 0, steps = 0, want = __shfl_sync(0xffffffffu, arg[0], 0);
 #pragma unroll
-    for (int k = 0; k < kTreeMaxNodes / 32; ++k) {
-      const int i = k * 32 + lane;
-      par[k] = (i > 0 && i < n) ? a.parents[base + i] : -1;
-      tok[k] = (i > 0 && i < n) ? a.tokens[base + i] : 0;
-    }
-    // path and tokens go out as they are found; the tails are filled afterwards
-    int cur = 0, steps = 0, want = ok ? a.argmax[base] : 0;
-    if (ok && lane == 0) a.path[base] = 0;
+    for (int k = 0; k < R; ++k) path[k] = com[k] = -1;
+    if (lane == 0) path[0] = 0;
     while (ok) {
       unsigned int best = 0xffffffffu;
 #pragma unroll
-      for (int k = kTreeMaxNodes / 32 - 1; k >= 0; --k) {
+      for (int k = R - 1; k >= 0; --k) {
         const int i = k * 32 + lane;
-        if (par[k] == cur && tok[k] == want && i > cur) best = (unsigned int)i;
+        if (par[k] == cur && tok[k] == want && i > cur && i < n) best = (unsigned int)i;
       }
       best = __reduce_min_sync(0xffffffffu, best);
       if (best == 0xffffffffu) break;
-      ++steps;
-      if (lane == 0) {
-        a.path[base + steps] = (int)best;
-        a.committed[base + steps - 1] = want;
+      int next = arg[0];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (steps == k * 32 + lane) com[k] = want;
+        if (steps + 1 == k * 32 + lane) path[k] = (int)best;
+        if ((int)best >> 5 == k) next = arg[k];
       }
+      ++steps;
       cur = (int)best;
-      want = a.argmax[base + cur];
+      want = __shfl_sync(0xffffffffu, next, cur & 31);
     }
     if (ok && (old < 0 || old > a.capacity - (steps + 1))) {  // no room: nothing of this sequence is committed
       if (lane == 0) set_status(a.status, old < 0 ? ORTHRUS_ERR_ARG : ORTHRUS_ERR_CAPACITY);
       ok = false;
     }
-    const int first = ok ? steps + 1 : 0;  // path entries kept
-    __syncwarp();
-    for (int i = lane; i < a.nodes; i += 32) {
-      if (i >= first) a.path[base + i] = -1;
-      if (i >= first) a.committed[base + i] = -1;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int i = k * 32 + lane;
+      if (i < a.nodes) {
+        a.path[base + i] = ok ? path[k] : -1;
+        a.committed[base + i] = !ok ? -1 : (i == steps ? want : com[k]);
+      }
     }
     if (lane == 0) {
-      if (ok) {
-        a.committed[base + steps] = want;
-        a.pending[b] = want;
-      }
+      if (ok) a.pending[b] = want;
       a.accept_len[b] = ok ? steps : -1;
       a.new_len[b] = ok ? old + steps + 1 : old;
     }
-    __syncwarp();
   }
 }
 
-// The path's K/V rows of one (layer, sequence, KV head), scratch row path[j] -> cache row
-// old + j, old = new_len - (a + 1). 16-byte pieces; source and destination are different buffers.
+// The path's K/V rows, scratch row path[j] -> cache row old + j, old = new_len - (a + 1). A CTA moves the rows of
+// `zs` (layer, KV head) pairs of one sequence in 16-byte pieces, two pairs of loads in flight a thread; source
+// and destination are different buffers. Bound by memory for a batch, by launch and three dependent loads for
+// one sequence.
 struct TreeMoveArgs {
   const uint4 *k_blk, *v_blk;
   uint4 *k_cache, *v_cache;
   const int *accept_len, *new_len, *path;
-  int batch, kv_heads, nodes, blk_stride, capacity, pieces;  // pieces: 16-byte pieces of a row
+  int layers, batch, kv_heads, nodes, blk_stride, capacity, pieces, zs;  // pieces: 16-byte pieces of a row
 };
 
-constexpr int kMoveThreads = 128;
+constexpr int kMoveThreads = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) tree_move_kernel(const TreeMoveArgs a) {
+  __shared__ int path[kTreeMaxNodes];
   griddep_wait();
   griddep_launch();
-  const int z = blockIdx.x;  // (layer * batch + b) * kv_heads + head
-  const int b = (z / a.kv_heads) % a.batch;
-  const int acc = a.accept_len[b];
+  const int b = blockIdx.y, acc = a.accept_len[b], old = a.new_len[b] - (acc + 1);
+  for (int i = threadIdx.x; i < a.nodes; i += kMoveThreads) path[i] = a.path[(size_t)b * a.nodes + i];
+  __syncthreads();
   if (acc < 0) return;
-  const int old = a.new_len[b] - (acc + 1);
-  const int total = (acc + 1) * a.pieces;
+  const int z0 = blockIdx.x * a.zs, zn = min(a.zs, a.layers * a.kv_heads - z0);
+  const int per = (acc + 1) * a.pieces, total = zn * per;
+#pragma unroll 2
   for (int i = threadIdx.x; i < total; i += kMoveThreads) {
-    const int j = i / a.pieces, c = i - j * a.pieces;
-    const int node = a.path[(size_t)b * a.nodes + j];
-    const size_t from = ((size_t)z * a.blk_stride + node) * a.pieces + c;
-    const size_t to = ((size_t)z * a.capacity + old + j) * a.pieces + c;
-    const uint4 k = a.k_blk[from], v = a.v_blk[from];
+    const int zi = i / per, r = i - zi * per, j = r / a.pieces, c = r - j * a.pieces;
+    const int layer = (z0 + zi) / a.kv_heads;
+    const size_t z = ((size_t)layer * a.batch + b) * a.kv_heads + (z0 + zi - layer * a.kv_heads);
+    const size_t from = (z * a.blk_stride + path[j]) * a.pieces + c, to = (z * a.capacity + old + j) * a.pieces + c;
+    const uint4 k = __ldcs(a.k_blk + from), v = __ldcs(a.v_blk + from);
     a.k_cache[to] = k;
     a.v_cache[to] = v;
   }
