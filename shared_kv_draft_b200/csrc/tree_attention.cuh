@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               ok = __all_sync(0xffffffffu, tree_wait(&ms.o_done[st], (cnt - 1) & 1, a.status));
               if (ok) {
                 tc_fence_after();
-                const float f = move ? exp2f(m - mt) : 1.f;
+                const float f = move ? fast_exp2(m - mt) : 1.f;
                 l *= f;
                 if (move) m = mt;
 #pragma unroll 1
@@ -634,8 +634,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const float2 ml0 = ms.ml[r];
         m = fmaxf(ml0.x, ml1.x);
         const float ref = m == -INFINITY ? 0.f : m;
-        w0 = exp2f(ml0.x - ref);
-        w1 = exp2f(ml1.x - ref);
+        w0 = fast_exp2(ml0.x - ref);
+        w1 = fast_exp2(ml1.x - ref);
         l = ml0.y * w0 + ml1.y * w1;
         e0 = st ? D / 2 : 0;
         e1 = st ? D : D / 2;
@@ -851,12 +851,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // 4 columns of each of E column groups), in key order:
 //     out = sum_c w_c O_c / sum_c w_c l_c,   w_c = 2^(m_c - max m),
 // P parts at a time with a running maximum, all their loads in flight together. Bound by the latency of
-// two dependent loads from L2 (notes, parts) and the wait for the first kernel: E x P = 16 loads a thread.
+// two dependent loads from L2 (notes, parts), the wait for the first kernel, and fetching its own code: with
+// E = 1, P = 16 instead of 8 takes 2 us longer at 18 parts.
 constexpr int kJoinThreads = 256;
 
 template <int E>
 __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAttnArgs a, int sms) {
-  constexpr int P = 16 / E;
+  constexpr int P = E == 1 ? 8 : 16 / E;
   __shared__ int before[kJoinThreads / 32];
   __shared__ int4 found;
   __shared__ int found_at;
@@ -914,7 +915,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAt
     float next = top;
 #pragma unroll
     for (int i = 0; i < P; ++i) next = fmaxf(next, m[i].x);
-    const float ref = next == -INFINITY ? 0.f : next, f = exp2f(top - ref);
+    const float ref = next == -INFINITY ? 0.f : next, f = fast_exp2(top - ref);
     top = next;
     l *= f;
 #pragma unroll
@@ -922,7 +923,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const TreeAt
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (i0 + i < n) {
-        const float w = exp2f(m[i].x - ref);
+        const float w = fast_exp2(m[i].x - ref);
         l += m[i].y * w;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
