@@ -295,6 +295,7 @@ orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_par
     a.heads += parts[i].heads;
     a.per_group[i] = (uint32_t)(((1ull << 32) + parts[i].group - 1) / parts[i].group);
   }
+  if (a.heads > 16384) return ORTHRUS_ERR_UNSUPPORTED;  // the reciprocals' products stay exact
   a.per_heads = (uint32_t)(((1ull << 32) + a.heads - 1) / a.heads);
   a.units = rope->head_dim / (vec ? 16 : 2);
   a.slots = kRotaryThreads / a.units;
