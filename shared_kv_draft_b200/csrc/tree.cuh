@@ -107,20 +107,26 @@ __global__ void __launch_bounds__(kWalkThreads) tree_walk_kernel(const TreeWalkA
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
-  const bool failed = a.status && *(volatile const int*)a.status != 0;
-  __syncthreads();
-  for (int b = threadIdx.x >> 5; b < a.batch; b += blockDim.x >> 5) {
+  bool failed = false;
+  const int laps = (a.batch + (blockDim.x >> 5) - 1) / (blockDim.x >> 5);
+  for (int lap = 0; lap < laps; ++lap) {
+    const int b = lap * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const bool mine = b < a.batch;
     const size_t base = (size_t)b * a.nodes;
     int par[R], tok[R], arg[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const int i = k * 32 + lane;
-      par[k] = i < a.nodes ? a.parents[base + i] : -1;
-      tok[k] = i < a.nodes ? a.tokens[base + i] : 0;
-      arg[k] = i < a.nodes ? a.argmax[base + i] : 0;
+      const bool in = mine && i < a.nodes;
+      par[k] = in ? a.parents[base + i] : -1;
+      tok[k] = in ? a.tokens[base + i] : 0;
+      arg[k] = in ? a.argmax[base + i] : 0;
     }
-    const int old = a.len[b];
-    int n = a.n_nodes ? a.n_nodes[b] : a.nodes;
+    const int old = mine ? a.len[b] : 0;
+    int n = mine ? (a.n_nodes ? a.n_nodes[b] : a.nodes) : 0;
+    // the status word once, before any sequence of the call can change it
+    if (lap == 0) failed = __syncthreads_or(a.status && *(volatile const int*)a.status != 0);
+    if (!mine) continue;
     bool ok = !failed && n > 0;
     if (n < 0 || n > a.nodes) {
       if (lane == 0) set_status(a.status, ORTHRUS_ERR_ARG);

@@ -318,6 +318,12 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 __device__ __forceinline__ float max3(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
 
 // Ring positions of a segment's tiles: `ahead` tiles of K, then V and K in turn.
@@ -699,7 +705,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---- loads: K and V in the order of their use, and q when the first K tiles are on their way (they
       // fill free stages while the last segment's scores still read its q) ----
       if (lane == 0 && ok) {
-        const uint64_t once = policy_evict_first();  // K and V are read once; the parts of cut units stay in L2
+        // one row group: K and V are read once, and the parts of cut units stay in L2; several: the other
+        // groups' CTAs read the same tiles
+        const uint64_t once = a.N * a.G > kTreeRows ? policy_evict_normal() : policy_evict_first();
         const int z = g.b * a.Hkv + g.kvh, lead = min(ahead, nt);
 #pragma unroll 1
         for (int p = 0; p < 2 * nt; ++p) {
