@@ -431,8 +431,8 @@ enum { ORTHRUS_FP32 = 0, ORTHRUS_BF16 = 1, ORTHRUS_FP16 = 2, ORTHRUS_BF16_PLANES
  * number of edges to the root; mask: uint64 [batch][nodes][(nodes + 63) / 64], bit
  * j % 64 of word j / 64 set iff node i sees node j (itself and its ancestors).
  * Padding nodes get depth 0 and no bits. A parent outside [-1, i) sets the device
- * status ORTHRUS_ERR_ARG (nullable) and counts as a root, and so does an n_nodes[b]
- * outside [0, nodes], which is clamped. Errors: ORTHRUS_ERR_ARG. */
+ * status word (nullable) to ORTHRUS_ERR_ARG and counts as a root; so does an n_nodes[b]
+ * outside [0, nodes], which is clamped. Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_CUDA. */
 orthrus_status orthrus_tree_layout(const int32_t* parents, const int32_t* n_nodes, int32_t batch, int32_t nodes,
                                    int32_t* depth, uint64_t* mask, int32_t* status, orthrus_stream stream);
 
@@ -448,8 +448,10 @@ orthrus_status orthrus_tree_layout(const int32_t* parents, const int32_t* n_node
  *            ORTHRUS_BF16_PLANES [2][batch*nodes][H*d] (token-major, head h at columns h*d..).
  * Rows of padding nodes are left as they were. A row that sees nothing (an empty
  * cache and no bits) is zero. Rows that no node sees may hold anything, NaN included.
- * A len[b] outside [0, capacity] sets the status and is clamped. Softmax statistics and sums are fp32; the
- * softmax weights are rounded to `type` for their product with V.
+ * A len[b] outside [0, capacity] sets the status (ORTHRUS_ERR_ARG, ORTHRUS_ERR_CAPACITY) and is clamped; an
+ * n_nodes[b] outside [0, nodes] is clamped. Softmax statistics and sums are fp32; the
+ * softmax weights are rounded to `type` for their product with V. Equal calls give equal bits; the same
+ * sequence in another batch may round differently (its keys are divided by the lengths of all).
  * 1 <= G <= 32, d in {64, 128}; q, K, V and out 16-byte aligned, mask 8-byte. The scratch
  * (orthrus_tree_attention_workspace_bytes, at most 64 MiB, 256-byte aligned) needs no initialisation and is
  * free again when the call's kernels are done; calls that may overlap on the GPU
@@ -474,7 +476,8 @@ orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const 
  *   new_len[b] = len[b] + a + 1 (may be the same array as len).
  * In every layer and KV head, scratch row path[j] of k_blk and v_blk
  * ([n_layers][batch][Hkv][blk_stride][d]) is copied to cache row len[b] + j
- * ([n_layers][batch][Hkv][capacity][d]), j = 0..a; the buffers must not overlap. Elements are
+ * ([n_layers][batch][Hkv][capacity][d]), j = 0..a. Outputs and inputs must not overlap but for len and
+ * new_len. Elements are
  * 16 bits wide, d a multiple of 8, the four buffers 16-byte aligned. A sequence without
  * room (len + a + 1 > capacity: status ORTHRUS_ERR_CAPACITY), an idle one (n_nodes[b] = 0), or any
  * while the status word holds an error commits nothing: accept_len = -1, path and committed all -1,
@@ -564,7 +567,7 @@ enum {
  * angles with the same gain: the gradient with respect to the heads. Angles are
  * formed in fp64, the rotation in fp32. Any strides and element-aligned pointers are
  * taken; 16-byte accesses are used where they allow it. batch or tokens 0 is nothing to
- * do. Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_CUDA. */
+ * do. At most 16384 heads in all (ORTHRUS_ERR_UNSUPPORTED). Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_CUDA. */
 orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_part* parts, int32_t n_parts,
                               int32_t batch, int32_t tokens, const int32_t* len, const int32_t* offsets,
                               int32_t inverse, int32_t* status, orthrus_stream stream);

@@ -162,10 +162,14 @@ bool ensure_smem_attr(F* kernel, size_t bytes) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const std::pair<int, const void*> key(dev, (const void*)kernel);
-  std::lock_guard<std::mutex> lock(mu);
-  if (std::find(done.begin(), done.end(), key) != done.end()) return true;
-  if (!set_smem_attr(kernel, bytes)) return false;
-  done.push_back(key);
+  try {  // no exception leaves a C entry point
+    std::lock_guard<std::mutex> lock(mu);
+    if (std::find(done.begin(), done.end(), key) != done.end()) return true;
+    if (!set_smem_attr(kernel, bytes)) return false;
+    done.push_back(key);
+  } catch (...) {
+    return false;
+  }
   return true;
 }
 

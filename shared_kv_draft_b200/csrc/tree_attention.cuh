@@ -6,25 +6,30 @@
 // in one pass over the keys with a running reference m per row; a row that sees nothing
 // gives zeros.
 //
-// Bound: the cache is read once, so HBM for trees of up to 256 rows (nodes x group) per KV
-// head; at 256 rows the two matrix products need as long as the reads.
+// Bound: every key is read once for up to 256 rows (nodes x group) of a KV head: HBM. At 256 rows
+// the two products (4 x 256 x d flops a key) need as long as the reads, and the exponentials,
+// 16 a cycle and SM, four fifths of that. Measured at d = 128: 128 rows or fewer 5.4 TB/s over
+// a long cache (8 sequences of 16384 keys, 16 nodes x 4: 99 us, 83% of the copy rate); 256 rows
+// 3.7 TB/s and 0.93 PFLOP/s (4 of 32768 keys, 64 x 4: 147 us). Short caches are bound by latency:
+// launch, first loads, two or three tiles, and the second kernel.
 //
-// Split. A unit is (sequence, KV head, group of up to 256 rows); its keys come in tiles of
-// 128, cache tiles first, then the tree's. All tiles of all units form one line, cut into
-// equal contiguous ranges, one per CTA and at most one CTA per SM: a ragged batch loads
-// every SM alike, with lengths known only on the device. A unit that lies in one range is
-// finished there; of a unit that is cut, each CTA stores its part (unnormalised sums, the
-// reference and the weights' sum per row, fp32), and tree_combine_kernel joins the parts in
-// key order. The cut depends on the lengths alone, so results repeat bit for bit.
+// Split. A unit is (sequence, KV head, group of up to 256 rows); its keys come in tiles of 64, cache
+// tiles first, then the tree's. The grid is a CTA an SM, and the lengths are on the device only,
+// so the CTAs divide the units by themselves (TreeShare below), by the tiles' costs: a ragged
+// batch loads every SM alike. A unit that one CTA has is finished there; of a unit that is cut,
+// each CTA stores its part (unnormalised sums, the reference and the weights' sum per row, fp32),
+// and tree_combine_kernel joins the parts in key order. The cuts follow from the lengths and sizes
+// of the call, so results repeat bit for bit.
 //
-// One CTA: warp 8 loads (TMA, ring of 128-key K and V tiles), warp 9 issues the MMAs, warps
-// 0-3 and 4-7 are two softmax streams, one thread per row. TMEM holds S0, S1 (128 columns
-// each) and O0, O1; P (16 bit) overwrites its S and is read by the second product from there.
+// One CTA: warp 8 loads (TMA, a ring of 160 KB in K and V tiles), warps 9 and 10 issue the MMAs, warps
+// 0-3 and 4-7 are two softmax streams, one thread per row. TMEM holds two S buffers of 64 columns and
+// the O of each stream; P (16 bit) overwrites its S and is read by the second product from there, so
+// that shared memory is left to the ring. While the softmax works on one buffer, the next scores
+// are written to the other.
 //   More than 128 rows: stream s owns rows [128 s, 128 s + 128) of the group and sees every
 //   tile, so a K/V tile is loaded once for both.
 //   At most 128 rows: both streams own the same rows and take the tiles in turn; their sums
 //   are joined when the segment ends.
-// Either way one stream's softmax runs under the other's products.
 //
 // The accumulators stay in TMEM. The reference m of a row moves only when a tile's maximum
 // exceeds it by more than 8 (a factor of 256), and only then is O rescaled. Weights carry a
@@ -46,9 +51,9 @@ namespace orthrus {
 
 constexpr int kTreeThreads = 384;  // 8 softmax warps, a load warp, two MMA warps, a note warp
 constexpr int kTreeKeys = 64;      // keys of a tile: one visibility word
-constexpr int kTreeRows = 256;      // rows of a unit
-constexpr float kTreeSlack = 8.f;   // how far scores may exceed the reference (log2)
-constexpr float kTreeShift = 7.f;   // factor on the weights (log2)
+constexpr int kTreeRows = 256;     // rows of a unit
+constexpr float kTreeSlack = 8.f;  // how far scores may exceed the reference (log2)
+constexpr float kTreeShift = 7.f;  // factor on the weights (log2)
 constexpr int kTreeLoadWarp = 8, kTreeMmaWarp = 9, kTreeNoteWarp = 11;  // MMA warps 9 and 10
 
 template <int D>
@@ -63,7 +68,9 @@ struct TreeSmem {
 };
 
 struct TreeMisc {
-  uint64_t full[20], empty[20], q_full, q_empty, s_full[4], p_full[4], o_done[2], done[2], seg_done;  // s_full, p_full: 2 stream + buffer
+  uint64_t full[20], empty[20], q_full, q_empty;
+  uint64_t s_full[4], p_full[4];  // [2 stream + buffer]
+  uint64_t o_done[2], done[2], seg_done;
   uint32_t tmem;
   int bad_any;
   unsigned int bad[8];  // tree rows with values that are not finite (this segment)
@@ -73,10 +80,15 @@ static_assert(sizeof(TreeMisc) <= 2048, "misc area");
 
 // ---- who works on what ------------------------------------------------------------------
 
-constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile's relative time with up to 128 rows, with more
-constexpr int kTreeUnit = 8;                   // and that of a unit: pipeline filled and drained, sums stored
+// Relative times, in steps of about 0.4 us. A tile took 0.78 us with up to 128 rows (bound by its reads) and
+// 1.06 us with 256; 3 : 4 instead of 2 : 3 cost 7% at 16 ragged sequences. What a unit costs beside its tiles
+// (pipeline filled and drained, sums stored) is about 3 us: 4 cost 6% there, 6 2%, 10 nothing.
+constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile with up to 128 rows, with more
+constexpr int kTreeUnit = 8;                   // a unit
 constexpr int kTreeSwitch = 10;                // how much longer than a range the even division's parts may be
-constexpr int kTreeMinTiles = 3;               // even division: tiles of a part at least
+// Tiles of a part at least, in the even division: more parts are quicker to compute and slower to join. One
+// sequence of 1024 keys: 12.8 us with 2, 13.4 with 3, 13.8 with 4; a tree step of 100 keys 10.2, 8.5, 8.4.
+constexpr int kTreeMinTiles = 3;
 
 struct TreeSeq {
   int n, live, tiles, groups, big;  // clamped length, nodes, tiles of a unit, row groups, groups of more than 128 rows
@@ -101,8 +113,8 @@ struct TreeSeq {
 // The division of the work. Even: every unit is cut into parts of its own, about as many as its share of
 // the CTAs, and a CTA has one part. Line: the costs of all units form one line, cut into ranges of equal
 // length, and a CTA has the tiles that start in its range, of one or several units (a unit's own cost lies
-// with its first tile). The even division is
-// taken where its largest part does not exceed the range by more than a switch of units costs.
+// with its first tile). The even division is taken where its largest part does not exceed a range by more than
+// kTreeSwitch: with few units a CTA then never changes from one to another.
 // (All costs fit 31 bits, which the host checks with the capacity.)
 struct TreeShare {
   int total, ctas, each, more;  // line
@@ -465,7 +477,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const uint32_t tmem = ms.tmem;
 
   // of every role: segments, ring position of the segment (tiles go through the ring in the order of
-  // their use: `ahead` tiles of K, then V and K in turn), and a wait that ran out
+  // their use: `ahead` tiles of K, then V and K in turn), and whether no wait has run out
   uint32_t seg = 0, base = 0;
   bool ok = true;
   // MMA warps: jobs of each stream so far, and the last segment's kind

@@ -226,6 +226,40 @@ def test_attention_ragged_batch(t):
                   counts=[33, 20, 1, 0, 33, 32, 7], blk_stride=40)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_units_of_both_kinds(d):
+    """40 nodes x 8 heads are 320 rows, one unit of 256 rows and one of 64 for each KV head; with other sequences
+    of 1 to 39 nodes a CTA goes from units of more than 128 rows to smaller ones and back."""
+    B = 20
+    run_attention(B, 4, 8, 40, d, 1600, [(397 * b) % 1500 for b in range(B)], seed=20, counts=[40 - (b * 7) % 40 for b in range(B)])
+
+
+def test_attention_random_cases():
+    """Sizes, lengths, types and node counts drawn at random, everything dead poisoned."""
+    import random
+    rng = random.Random(23)
+    for _ in range(60):
+        d, G, N = rng.choice([64, 128]), rng.choice([1, 2, 3, 4, 5, 8, 16, 32]), rng.choice([1, 2, 7, 16, 33, 64, 65, 90, 130, 256])
+        B, H, most = rng.choice([1, 1, 2, 5, 20, 70]), rng.choice([1, 2, 3, 8]), rng.choice([0, 5, 70, 300, 1500])
+        if B * H * N * G * (most + N) > 3e8:
+            continue
+        lens = [rng.randint(0, most) for _ in range(B)]
+        counts = None if rng.random() < 0.4 else [rng.randint(0, N) for _ in range(B)]
+        a = make_attention(B, H, G, N, d, max(1, max(lens)) + rng.choice([0, 1, 50]), lens, seed=rng.randint(0, 10 ** 6),
+                           t=rng.choice([torch.float16, torch.bfloat16]), counts=counts, blk_stride=N + rng.choice([0, 3]))
+        for b in range(B):
+            live = N if counts is None else counts[b]
+            for x in (a["k_cache"], a["v_cache"]):
+                x[b, :, lens[b]:] = float("nan")
+            for x in (a["k_blk"], a["v_blk"]):
+                x[b, :, live:] = float("nan")
+            a["q"][b, :, live * G:] = float("nan")
+        planes = rng.random() < 0.3
+        out, status = call_attention(a, planes=planes)
+        assert int(status.item()) == 0
+        check_attention(a, out, planes)
+
+
 def test_attention_many_sequences():
     run_attention(200, 1, 2, 5, 64, 192, [(37 * b) % 180 for b in range(200)], seed=6, counts=[b % 6 for b in range(200)])
 

@@ -173,6 +173,9 @@ def test_rotary_refuses(lib):
     assert call(ref, part, 4, 1, 1) == orthrus.ERR_ARG
     assert call(ref, part, 1, -1, 1) == orthrus.ERR_ARG
     assert call(ref, part, 1, 1, -1) == orthrus.ERR_ARG
+    many = (orthrus.RotaryPart * 2)(rotary_part(heads=16384), rotary_part(heads=1))  # more than 16384 heads in all
+    assert call(ref, many, 2, 1, 1) == orthrus.ERR_UNSUPPORTED
+    assert call(ref, part, 1, 1 << 16, 1 << 16) == orthrus.ERR_ARG  # more than 2^31 - 1 tokens
     bad = orthrus.Rope(128, 130, 0, 1.0)
     assert call(C.byref(bad), part, 1, 1, 1) == orthrus.ERR_ARG
     assert call(ref, part, 1, 0, 5) == orthrus.OK and call(ref, part, 1, 5, 0) == orthrus.OK  # nothing to do
