@@ -1,4 +1,4 @@
-"""Build liborthrus.so (sm_100a) in-tree with nvcc.
+"""Build liborthrus.so (sm_100a, nvcc) and the native part of its Python binding (g++) in-tree.
 
     python -m shared_kv_draft_b200.build [--force]
 """
@@ -8,6 +8,7 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +17,8 @@ SRC_DIR = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "liborthrus.so")
 OBJ_DIR = os.path.join(HERE, "_build")  # object files, one per translation unit
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(SRC_DIR, "binding.cpp")
 UNITS = [os.path.join(SRC_DIR, u) for u in ("orthrus.cu", "operators.cu")]
 
 
@@ -29,15 +32,15 @@ def _nvcc() -> str:
 def sources():
     out = [os.path.join(INCLUDE, "orthrus.h")]
     for f in sorted(os.listdir(SRC_DIR)):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f.endswith((".cu", ".cuh", ".h", ".cpp")):
             out.append(os.path.join(SRC_DIR, f))
     return out
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
@@ -77,6 +80,19 @@ def _compile(src: str, force: bool, verbose: bool) -> str:
     return obj
 
 
+def _build_binding(verbose: bool) -> None:
+    """Python module over torch's headers, linked with liborthrus.so beside it."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda", "include"), sysconfig.get_paths()["include"]]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+         + [x for d in inc for x in ("-I", d)] + [BINDING_SRC, "-o", BINDING + ".tmp", "-L", HERE, "-l:liborthrus.so",
+                                                  "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"), "-ltorch_python",
+                                                  "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
@@ -86,6 +102,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     _run([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp"]
          + objs, verbose)
     os.replace(LIB + ".tmp", LIB)
+    _build_binding(verbose)
     return LIB
 
 

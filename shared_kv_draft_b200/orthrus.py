@@ -2,7 +2,9 @@
 
 Argument marshalling only: every computation runs in the library's sm_100a
 kernels. PyTorch provides device memory and the current CUDA stream. Loading
-fails loudly when the library has not been built; there is no fallback.
+fails loudly when the library has not been built; there is no fallback. The
+tree and rotary calls, which run once a layer and have many tensors to check,
+are marshalled by a native module (csrc/binding.cpp).
 
 The function names mirror the C entry points without the ``orthrus_`` prefix.
 ``DeviceModel`` owns the device buffers a plan needs (weights uploaded from
@@ -13,8 +15,6 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
-import struct
-from builtins import len as _length  # some calls below have an argument `len`, the cache lengths
 
 import numpy as np
 import torch
@@ -258,74 +258,23 @@ def linear_workspace_bytes(M, N, Kd) -> int:
 
 # ---- draft trees and rotary positions ------------------------------------------------------------
 
-_TYPES = {torch.float32: FP32, torch.bfloat16: BF16, torch.float16: FP16}
+_binding = None
 
 
-_PARTS = [struct.Struct("PPiiiiiiqqqqqqq" * n) for n in range(ROTARY_MAX_PARTS + 1)]  # orthrus_rotary_part [n]
-assert _PARTS[3].size == 3 * C.sizeof(RotaryPart)
-
-
-def _on(dev, stream):
-    """The raw stream of a call on device `dev`: `stream`, or the device's current one."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _call(dev, fn, *args):
-    """fn(*args) with `dev`, the device of the call's tensors, as the current device."""
-    now = torch._C._cuda_getDevice()
-    if now == dev:
-        code = fn(*args)
-    else:
-        torch.cuda.set_device(dev)
-        try:
-            code = fn(*args)
-        finally:
-            torch.cuda.set_device(now)
-    if code != OK:
-        raise OrthrusError(fn.__name__, code)
-
-
-def _arg(ok, call, what):
-    if not ok:
-        raise ValueError(f"{call}: {what}")
-
-
-def _refuse(call, dev, wanted):
-    """Raise for the first tensor of `wanted` (name, tensor, dtype, shape) that is not densely on device `dev` with
-    that dtype and shape. Called when the one-expression check of a call has failed."""
-    for name, t, dtype, shape in wanted:
-        if t is None or not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-                             and (shape is None or tuple(t.shape) == tuple(shape))):
-            raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor on device {dev}"
-                             + ("" if shape is None else f" of shape {tuple(shape)}"))
-    raise ValueError(f"{call}: the tensors do not fit one another")
-
-
-_I = torch.int32
-
-
-def _optional(call, dev, n, name, t):
-    """Address of an optional int32 array of n elements."""
-    if t is None:
-        return None
-    if not (t.dtype is _I and t.get_device() == dev and t.numel() == n and t.is_contiguous()):
-        _refuse(call, dev, [(name, t, _I, (n,))])
-    return t.data_ptr()
+def _native():
+    """The native module that checks the arguments of these calls and makes them (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        load()
+        from . import _binding as module  # fails loudly when it has not been built
+        _binding = module
+    return _binding
 
 
 def tree_layout(parents, depth, mask, n_nodes=None, status=None, stream=None):
     """Depths and visibility words of draft trees. parents: int32 [B][N]; depth: int32 [B][N]; mask:
     int64 [B][N][ceil(N / 64)] (the words' bits)."""
-    dev, name, shape = parents.get_device(), "tree_layout", parents.shape
-    _arg(dev >= 0 and _length(shape) == 2, name, "parents must be [batch][nodes] on a GPU")
-    B, N = shape
-    words = (B, N, (N + 63) // 64)
-    if not (parents.dtype is _I and parents.is_contiguous() and depth.dtype is _I and depth.get_device() == dev
-            and depth.is_contiguous() and depth.shape == shape and mask.dtype is torch.int64
-            and mask.get_device() == dev and mask.is_contiguous() and mask.shape == words):
-        _refuse(name, dev, [("parents", parents, _I, None), ("depth", depth, _I, shape), ("mask", mask, torch.int64, words)])
-    _call(dev, load().orthrus_tree_layout, parents.data_ptr(), _optional(name, dev, B, "n_nodes", n_nodes), B, N,
-          depth.data_ptr(), mask.data_ptr(), _optional(name, dev, 1, "status", status), _on(dev, stream))
+    _native().tree_layout(parents, depth, mask, n_nodes, status, stream)
 
 
 def tree_attention_workspace_bytes(batch, n_kv_heads, group, nodes, head_dim) -> int:
@@ -338,34 +287,7 @@ def tree_attention(q, k_cache, v_cache, k_blk, v_blk, len, mask, out, workspace,
     [B][Hkv][capacity][d]; k_blk, v_blk: [B][Hkv][>= N][d], all fp16 or all bf16; len: int32 [B]; mask: int64
     [B][N][words]; out: fp16 or bf16 [B*N][H*d], or bf16 [2][B*N][H*d] (hi and lo plane); workspace:
     tree_attention_workspace_bytes() or more."""
-    dev, t, name = q.get_device(), q.dtype, "tree_attention"
-    _arg(dev >= 0 and q.dim() == 4 and (t is torch.float16 or t is torch.bfloat16), name,
-         "q must be fp16 or bf16 [batch][kv heads][nodes*group][d] on a GPU")
-    B, H, R, d = q.shape
-    _arg(mask.dim() == 3 and mask.size(1) > 0, name, "mask must be [batch][nodes][words]")
-    N = mask.size(1)
-    G = R // N
-    _arg(G * N == R, name, "mask does not fit q")
-    _arg(k_cache.dim() == 4 and k_blk.dim() == 4 and k_blk.size(2) >= N, name, "a cache or block has another shape")
-    cap, rows, words = k_cache.size(2), k_blk.size(2), (B, N, (N + 63) // 64)
-    cs, bs = (B, H, cap, d), (B, H, rows, d)
-    planes, to = out.dim() == 3, out.dtype
-    os_ = (2, B * N, H * G * d) if planes else (B * N, H * G * d)
-    _arg(to is torch.bfloat16 or (to is torch.float16 and not planes), name, "out must be fp16 or bf16, planes bf16")
-    if not (q.is_contiguous() and k_cache.dtype is t and k_cache.get_device() == dev and k_cache.is_contiguous()
-            and k_cache.shape == cs and v_cache.dtype is t and v_cache.get_device() == dev and v_cache.is_contiguous()
-            and v_cache.shape == cs and k_blk.dtype is t and k_blk.get_device() == dev and k_blk.is_contiguous()
-            and k_blk.shape == bs and v_blk.dtype is t and v_blk.get_device() == dev and v_blk.is_contiguous()
-            and v_blk.shape == bs and mask.dtype is torch.int64 and mask.get_device() == dev and mask.is_contiguous()
-            and mask.shape == words and out.get_device() == dev and out.is_contiguous() and out.shape == os_
-            and len is not None and workspace.get_device() == dev and workspace.is_contiguous()):
-        _refuse(name, dev, [("q", q, t, None), ("k_cache", k_cache, t, cs), ("v_cache", v_cache, t, cs), ("k_blk", k_blk, t, bs),
-                            ("v_blk", v_blk, t, bs), ("mask", mask, torch.int64, words), ("out", out, to, os_),
-                            ("len", len, _I, (B,)), ("workspace", workspace, workspace.dtype, None)])
-    _call(dev, load().orthrus_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_blk.data_ptr(),
-          v_blk.data_ptr(), _optional(name, dev, B, "len", len), _optional(name, dev, B, "n_nodes", n_nodes), mask.data_ptr(),
-          B, H, G, N, d, cap, rows, _TYPES[t], BF16_PLANES if planes else _TYPES[to], scale, out.data_ptr(),
-          workspace.data_ptr(), workspace.nbytes, _optional(name, dev, 1, "status", status), _on(dev, stream))
+    _native().tree_attention(q, k_cache, v_cache, k_blk, v_blk, len, mask, out, workspace, n_nodes, scale, status, stream)
 
 
 def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, new_len, pending, accept_len, path,
@@ -373,36 +295,8 @@ def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, ne
     """Greedy consensus on draft trees and the accepted paths' K/V rows into the cache. k_blk, v_blk:
     [L][B][Hkv][>= N][d] and k_cache, v_cache: [L][B][Hkv][capacity][d] of one 16-bit type; the others int32, [B] or
     [B][N]. new_len may be len."""
-    dev, name, shape = parents.get_device(), "tree_commit", parents.shape
-    _arg(dev >= 0 and _length(shape) == 2 and k_cache.dim() == 5 and k_blk.dim() == 5, name,
-         "parents must be [batch][nodes] on a GPU, caches and blocks five-dimensional")
-    B, N = shape
-    t = k_cache.dtype
-    L, _, H, cap, d = k_cache.shape
-    rows = k_blk.size(3)
-    cs, bs = (L, B, H, cap, d), (L, B, H, rows, d)
-    if not (t.itemsize == 2 and rows >= N and parents.dtype is _I and parents.is_contiguous()
-            and tokens.dtype is _I and tokens.get_device() == dev and tokens.is_contiguous() and tokens.shape == shape
-            and argmax.dtype is _I and argmax.get_device() == dev and argmax.is_contiguous() and argmax.shape == shape
-            and path.dtype is _I and path.get_device() == dev and path.is_contiguous() and path.shape == shape
-            and committed.dtype is _I and committed.get_device() == dev and committed.is_contiguous()
-            and committed.shape == shape and k_cache.get_device() == dev and k_cache.is_contiguous()
-            and k_cache.shape == cs and v_cache.dtype is t and v_cache.get_device() == dev and v_cache.is_contiguous()
-            and v_cache.shape == cs and k_blk.dtype is t and k_blk.get_device() == dev and k_blk.is_contiguous()
-            and k_blk.shape == bs and v_blk.dtype is t and v_blk.get_device() == dev and v_blk.is_contiguous()
-            and v_blk.shape == bs and len is not None and new_len is not None and pending is not None
-            and accept_len is not None):
-        _refuse(name, dev, [("parents", parents, _I, None), ("tokens", tokens, _I, shape), ("argmax", argmax, _I, shape),
-                            ("path", path, _I, shape), ("committed", committed, _I, shape), ("k_cache", k_cache, t, cs),
-                            ("v_cache", v_cache, t, cs), ("k_blk", k_blk, t, bs), ("v_blk", v_blk, t, bs),
-                            ("len", len, _I, (B,)), ("new_len", new_len, _I, (B,)), ("pending", pending, _I, (B,)),
-                            ("accept_len", accept_len, _I, (B,))])
-    _call(dev, load().orthrus_tree_commit, parents.data_ptr(), tokens.data_ptr(), argmax.data_ptr(),
-          _optional(name, dev, B, "n_nodes", n_nodes), k_blk.data_ptr(), v_blk.data_ptr(), rows, k_cache.data_ptr(),
-          v_cache.data_ptr(), L, B, H, cap, d, N, _optional(name, dev, B, "len", len),
-          _optional(name, dev, B, "new_len", new_len), _optional(name, dev, B, "pending", pending),
-          _optional(name, dev, B, "accept_len", accept_len), path.data_ptr(), committed.data_ptr(),
-          _optional(name, dev, 1, "status", status), _on(dev, stream))
+    _native().tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, new_len, pending, accept_len, path,
+                          committed, n_nodes, status, stream)
 
 
 @functools.lru_cache(maxsize=64)
@@ -411,7 +305,8 @@ def rope(head_dim, rot_dim=None, theta=1.0e6, interleaved=False, scaling="none",
     """Frequencies of a rotary embedding (host only): the table for rotary(). The same arguments give the same
     table object; it is not to be changed (fill a Rope for frequencies of one's own)."""
     r = Rope()
-    _arg(scaling in ROPE_SCALINGS, "rope", f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"rope: scaling must be one of {sorted(ROPE_SCALINGS)}")
     _check("orthrus_rope_init",
            load().orthrus_rope_init(C.byref(r), head_dim, head_dim if rot_dim is None else rot_dim, int(bool(interleaved)),
                                     theta, ROPE_SCALINGS[scaling], factor, original, slow, fast, gain))
@@ -425,42 +320,7 @@ def rotary(rope, parts, len=None, offsets=None, inverse=False, status=None, stre
     [B][rows][kv heads][group][d]; views with any strides, the last dimension dense; fp32, bf16 or fp16.
     rows = T, or with ROTARY_APPEND the rows of the cache that rows len[b] + t are written to. ROTARY_COPY:
     no rotation; ROTARY_BF16_VALUES: rounded to bf16 first. inverse: back by the same angles (the gradient)."""
-    name, n, hd = "rotary", _length(parts), rope.head_dim
-    _arg(1 <= n <= ROTARY_MAX_PARTS, name, f"1 to {ROTARY_MAX_PARTS} parts")
-    first = parts[0][0]
-    dev = first.get_device()
-    _arg(dev >= 0 and first.dim() == 4, name, "src must be [batch][tokens][heads][d] on a GPU")
-    B, T = first.size(0), first.size(1)
-    values = []
-    for part in parts:
-        src, dst = part[0], part[1]
-        flags = part[2] if _length(part) > 2 else 0
-        ss, ds, sh, dh = src.stride(), dst.stride(), src.shape, dst.shape
-        a, b, nd = _TYPES.get(src.dtype), _TYPES.get(dst.dtype), _length(dh)
-        if not (a is not None and b is not None and src.get_device() == dev and dst.get_device() == dev):
-            raise ValueError("rotary: tensors must be fp32, bf16 or fp16 on one GPU")
-        if not (_length(sh) == 4 and sh[0] == B and sh[1] == T and sh[3] == hd and ss[3] == 1):
-            raise ValueError("rotary: src must be [batch][tokens][heads][d] with a dense last dimension")
-        if nd == 4:
-            group, heads, inner = 1, dh[2], 0
-        elif nd == 5:
-            group, heads, inner = dh[3], dh[2] * dh[3], ds[3]
-        else:
-            group = heads = inner = 0
-        if not (heads == sh[2] and dh[0] == B and dh[-1] == hd and ds[-1] == 1 and (flags & ROTARY_APPEND or dh[1] == T)):
-            raise ValueError("rotary: dst must be [batch][rows][heads][d] or [batch][rows][kv heads][group][d] with a "
-                             "dense last dimension")
-        values += (src.data_ptr(), dst.data_ptr(), a, b, heads, group, flags, dh[1], ss[0], ss[1], ss[2], ds[0], ds[1],
-                   ds[2], inner)
-    off = None
-    if offsets is not None:
-        if not (offsets.dtype is _I and offsets.get_device() == dev and offsets.is_contiguous()
-                and offsets.shape == (B, T)):
-            _refuse(name, dev, [("offsets", offsets, _I, (B, T))])
-        off = offsets.data_ptr()
-    _call(dev, load().orthrus_rotary, C.addressof(rope), _PARTS[n].pack(*values), n, B, T,
-          _optional(name, dev, B, "len", len), off, 1 if inverse else 0, _optional(name, dev, 1, "status", status),
-          _on(dev, stream))
+    _native().rotary(rope, parts, len, offsets, inverse, status, stream)
 
 
 # ---- a plan with its device buffers --------------------------------------------------------------
