@@ -387,9 +387,28 @@ __device__ __forceinline__ uint32_t tree_pack(float x, float y) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ bool tree_finite(uint32_t bits) {  // both 16-bit values
+__device__ __forceinline__ bool tree_finite(uint16_t bits) {
   constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
-  return (bits & e) != e && (bits >> 16 & e) != e;
+  return (bits & e) != e;
+}
+
+// All eight: x 0 summed is zero, or NaN where a value is not finite.
+template <bool BF16>
+__device__ __forceinline__ bool tree_all_finite(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (BF16) {
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 s = zero;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), zero, s);
+    return __hbeq2(s, zero);
+  } else {
+    const __half2 zero = __floats2half2_rn(0.f, 0.f);
+    __half2 s = zero;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __hfma2(*reinterpret_cast<const __half2*>(&w[i]), zero, s);
+    return __hbeq2(s, zero);
+  }
 }
 
 // values out[at .. at + 8) of one row
@@ -526,39 +545,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         const bool part = blk || lim < kTreeKeys;
         if (part) {
-          // thread r < 64 looks after key r: V rows that nobody may see become zero, and values that are not
-          // finite are marked and leave the product. With two streams on the tile both do it: each one's
-          // products follow its own pass, and the later one finds values already marked. A row is 128 bytes
-          // of each half: the threads start at different 16 bytes of theirs, on different banks. (The wait is
-          // after that for the scores: then the stage's earlier laps are over, and its parity is this lap's.)
+          // thread r looks after half of key r & 63: V rows that nobody may see become zero, and values that are
+          // not finite are marked and leave the product. With two streams on the tile both do it: each one's
+          // products follow its own pass, and the later one finds values already marked. A key's row is 128
+          // bytes of each half of the columns: the threads start at different 16 bytes of theirs, on different
+          // banks. (The wait is after that for the scores: then the stage's earlier laps are over, and its parity
+          // is this lap's.)
           const uint32_t pos = base + tree_pos_v(k, ahead, nt), s = pos % S::kStages;
           if (ok) ok = tree_wait(&ms.full[s], (pos / S::kStages) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
-          if (ok && r < kTreeKeys) {
-            uint4* vr = reinterpret_cast<uint4*>(ring + s * S::kTile + r * 128);
-            bool bad = false;
-            if (r < lim && blk) {
-#pragma unroll 4
-              for (int q = 0; q < 8 * kHalves; ++q) {
-                const uint4 x = vr[(q >> 3) * (kHalf / 16) + ((q + r) & 7)];
-                bad = bad || !(tree_finite<BF16>(x.x) && tree_finite<BF16>(x.y) && tree_finite<BF16>(x.z) &&
-                               tree_finite<BF16>(x.w));
-              }
-            }
-            if (bad) {
-              const int j = bt * kTreeKeys + r;
-              atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
-              ms.bad_any = 1;
-              __threadfence_block();
+          if (ok) {
+            const int key = r & 63, q0 = (r >> 6) * 4 * kHalves;
+            uint4* vr = reinterpret_cast<uint4*>(ring + s * S::kTile + key * 128);
+            auto piece = [&](int q) -> uint4& { return vr[((q0 + q) >> 3) * (kHalf / 16) + ((q0 + q + key) & 7)]; };
+            if (key >= lim) {
+#pragma unroll
+              for (int q = 0; q < 4 * kHalves; ++q) piece(q) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (blk) {
+              bool fine = true;
+#pragma unroll
+              for (int q = 0; q < 4 * kHalves; ++q) fine = fine && tree_all_finite<BF16>(piece(q));
+              if (!fine) {
+                const int j = bt * kTreeKeys + key;
+                atomicOr(&ms.bad[j >> 5], 1u << (j & 31));
+                ms.bad_any = 1;
+                __threadfence_block();
 #pragma unroll 1
-              for (int q = 0; q < 64 * kHalves; ++q) {
-                uint16_t* x = reinterpret_cast<uint16_t*>(vr) + (q >> 6) * (kHalf / 2) + (q & 63);
-                if (!tree_finite<BF16>(*x)) *x = 0;
+                for (int q = 0; q < 32 * kHalves; ++q) {
+                  uint16_t* x = reinterpret_cast<uint16_t*>(&piece(q >> 3)) + (q & 7);
+                  if (!tree_finite<BF16>(*x)) *x = 0;
+                }
               }
-            }
-            if (r >= lim) {
-#pragma unroll 4
-              for (int q = 0; q < 8 * kHalves; ++q) vr[(q >> 3) * (kHalf / 16) + ((q + r) & 7)] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
           }
