@@ -30,7 +30,7 @@ struct RotaryArgs {
   float gain;
   int batch, tokens, tok_per_cta;
   int heads;               // of all parts
-  uint32_t per_heads;      // ceil(2^32 / heads)
+  uint32_t per_heads;      // ceil(2^32 / heads); one head has none (2^32)
   int units, slots;        // units of a head, heads that a CTA has in hand at a time
   const int* len;
   const int* offsets;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
   if (slot >= a.slots) return;
 #pragma unroll 2
   for (int i = blockIdx.y * a.slots + slot; i < nt * a.heads; i += gridDim.y * a.slots) {
-    const int k = (int)__umulhi((uint32_t)i, a.per_heads);
+    const int k = a.heads == 1 ? i : (int)__umulhi((uint32_t)i, a.per_heads);
     int h = i - k * a.heads, j = 0;
     while (h >= a.part[j].heads) h -= a.part[j++].heads;
     const orthrus_rotary_part& p = a.part[j];

@@ -94,6 +94,17 @@ def test_sizes(B, T, H, Hkv):
     check(yk, k, pos, rope)
 
 
+@pytest.mark.parametrize("d", [128, 20])
+@pytest.mark.parametrize("T", [2367, 2368, 5000, 20001])
+def test_one_head_of_many_tokens(T, d):
+    o = lib()
+    rope = o.rope(d)
+    x = normal((1, T, 1, d), B16, 18)
+    y = torch.empty_like(x)
+    o.rotary(rope, [(x, y)])
+    check(y, x, torch.arange(T)[None], rope)
+
+
 @pytest.mark.parametrize("scaling", ["none", "linear", "by_parts", "by_index"])
 def test_far_positions_and_stretched_contexts(scaling):
     """Positions up to 16 million, negative ones among them."""
