@@ -268,7 +268,8 @@ orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_par
   bool vec = rope->head_dim % 16 == 0 && rope->rot_dim % 16 == 0;
   for (int i = 0; i < n_parts; ++i) {
     const orthrus_rotary_part& p = parts[i];
-    if (!p.src || !p.dst || p.heads < 1 || p.group < 1 || p.heads % p.group || p.heads > 65536) return ORTHRUS_ERR_ARG;
+    if ((!p.src || !p.dst) && batch > 0 && tokens > 0) return ORTHRUS_ERR_ARG;  // an empty tensor may have no memory
+    if (p.heads < 1 || p.group < 1 || p.heads % p.group || p.heads > 65536) return ORTHRUS_ERR_ARG;
     for (const int t : {p.src_type, p.dst_type})
       if (t != ORTHRUS_FP32 && t != ORTHRUS_BF16 && t != ORTHRUS_FP16) return ORTHRUS_ERR_ARG;
     if (p.flags & ~(ORTHRUS_ROTARY_COPY | ORTHRUS_ROTARY_APPEND | ORTHRUS_ROTARY_BF16_VALUES)) return ORTHRUS_ERR_ARG;

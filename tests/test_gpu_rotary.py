@@ -94,6 +94,15 @@ def test_sizes(B, T, H, Hkv):
     check(yk, k, pos, rope)
 
 
+@pytest.mark.parametrize("B,T", [(0, 5), (2, 0)])
+def test_no_tokens(B, T):
+    o = lib()
+    x, cache = normal((B, T, 4, 64), B16, 19), torch.zeros((B, 8, 4, 64), device="cuda")
+    y = torch.empty_like(x)
+    o.rotary(o.rope(64), [(x, y), (x, cache, o.ROTARY_APPEND)], len=torch.zeros(B, dtype=torch.int32, device="cuda"))
+    assert not cache.any()
+
+
 @pytest.mark.parametrize("d", [128, 20])
 @pytest.mark.parametrize("T", [2367, 2368, 5000, 20001])
 def test_one_head_of_many_tokens(T, d):

@@ -179,6 +179,9 @@ def test_rotary_refuses(lib):
     bad = orthrus.Rope(128, 130, 0, 1.0)
     assert call(C.byref(bad), part, 1, 1, 1) == orthrus.ERR_ARG
     assert call(ref, part, 1, 0, 5) == orthrus.OK and call(ref, part, 1, 5, 0) == orthrus.OK  # nothing to do
+    empty = (orthrus.RotaryPart * 1)(rotary_part(src=None, dst=None))
+    assert call(ref, empty, 1, 0, 5) == orthrus.OK and call(ref, empty, 1, 5, 0) == orthrus.OK
+    assert call(ref, empty, 1, 1, 1) == orthrus.ERR_ARG
 
 
 # ---- the binding's checks (tensors on the CPU are refused before anything else) ------------------------
