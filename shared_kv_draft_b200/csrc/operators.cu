@@ -276,6 +276,10 @@ orthrus_status orthrus_rotary(const orthrus_rope* rope, const orthrus_rotary_par
     if ((p.flags & ORTHRUS_ROTARY_APPEND) && p.rows < 1) return ORTHRUS_ERR_ARG;
     if (!aligned(p.src, p.src_type == ORTHRUS_FP32 ? 4 : 2) || !aligned(p.dst, p.dst_type == ORTHRUS_FP32 ? 4 : 2))
       return ORTHRUS_ERR_ARG;
+    // values that would be written to one place (a broadcast destination)
+    if ((!p.dst_batch && batch > 1) || (!p.dst_token && tokens > 1) || (!p.dst_kv && p.heads > p.group) ||
+        (!p.dst_head && p.group > 1))
+      return ORTHRUS_ERR_ARG;
     vec = vec && aligned(p.src, 16) && aligned(p.dst, 16);
     for (const int64_t s : {p.src_batch, p.src_token, p.src_head, p.dst_batch, p.dst_token, p.dst_kv, p.dst_head})
       vec = vec && s % 8 == 0;

@@ -103,6 +103,18 @@ def test_no_tokens(B, T):
     assert not cache.any()
 
 
+def test_broadcast_source_and_destination():
+    o = lib()
+    rope = o.rope(64)
+    x = normal((1, 1, 2, 64), F32, 20).expand(3, 5, 2, 64)
+    y = torch.empty((3, 5, 2, 64), device="cuda")
+    o.rotary(rope, [(x, y)])
+    check(y, x, torch.arange(5).expand(3, 5), rope)
+    for flat in (y[:1].expand(3, 5, 2, 64), y[:, :1].expand(3, 5, 2, 64), y[:, :, :1].expand(3, 5, 2, 64)):
+        with pytest.raises(o.OrthrusError):
+            o.rotary(rope, [(y.clone(), flat)])
+
+
 @pytest.mark.parametrize("d", [128, 20])
 @pytest.mark.parametrize("T", [2367, 2368, 5000, 20001])
 def test_one_head_of_many_tokens(T, d):

@@ -156,7 +156,7 @@ def rotary_part(**kw):
 @pytest.mark.parametrize("bad", [
     dict(src=None), dict(dst=None), dict(heads=0), dict(group=0), dict(group=3), dict(src_type=3), dict(dst_type=-1),
     dict(flags=8), dict(flags=orthrus.ROTARY_APPEND, rows=0), dict(heads=65537), dict(src=C.c_void_p(1025)),
-    dict(src=ODD), dict(dst=C.c_void_p(1025))], ids=str)
+    dict(src=ODD), dict(dst=C.c_void_p(1025)), dict(dst_kv=0), dict(group=2)], ids=str)
 def test_rotary_refuses_a_part(lib, bad):
     rope = orthrus.rope(128)
     part = (orthrus.RotaryPart * 1)(rotary_part(**bad))
@@ -179,6 +179,9 @@ def test_rotary_refuses(lib):
     bad = orthrus.Rope(128, 130, 0, 1.0)
     assert call(C.byref(bad), part, 1, 1, 1) == orthrus.ERR_ARG
     assert call(ref, part, 1, 0, 5) == orthrus.OK and call(ref, part, 1, 5, 0) == orthrus.OK  # nothing to do
+    flat = (orthrus.RotaryPart * 2)(rotary_part(dst_batch=0), rotary_part(dst_token=0))  # broadcast destinations
+    assert call(ref, C.byref(flat, 0), 1, 2, 1) == orthrus.ERR_ARG
+    assert call(ref, C.byref(flat, C.sizeof(orthrus.RotaryPart)), 1, 1, 2) == orthrus.ERR_ARG
     empty = (orthrus.RotaryPart * 1)(rotary_part(src=None, dst=None))
     assert call(ref, empty, 1, 0, 5) == orthrus.OK and call(ref, empty, 1, 5, 0) == orthrus.OK
     assert call(ref, empty, 1, 1, 1) == orthrus.ERR_ARG
