@@ -70,7 +70,7 @@ struct TreeSmem {
 struct TreeMisc {
   uint64_t full[20], empty[20], q_full, q_empty;
   uint64_t s_full[4], p_full[4];  // [2 stream + buffer]
-  uint64_t o_done[2], done[2], seg_done;
+  uint64_t o_done[2], o_last[2], done[2], seg_done;
   uint32_t tmem;
   int bad_any;
   unsigned int bad[8];  // tree rows with values that are not finite (this segment)
@@ -475,6 +475,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     mbar_init(&ms.o_done[0], 1);
     mbar_init(&ms.o_done[1], 1);
+    mbar_init(&ms.o_last[0], 1);
+    mbar_init(&ms.o_last[1], 1);
     mbar_init(&ms.seg_done, 2);
     mbar_init(&ms.done[0], 1);
     mbar_init(&ms.done[1], 1);
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   bool was_two = false;
   // softmax: stream, row of the 128, jobs so far
   const int st = warp >> 2, r = (warp & 3) * 32 + lane;
-  uint32_t cnt = 0;
+  uint32_t cnt = 0, ends = 0;  // and segments in which the stream had a job
   // note warp: the unit's cost before the range (line)
   const int skipped = walk.left - (share.at(blockIdx.x + 1) - share.at(blockIdx.x));
   int4 note = make_int4(-1, 0, 0, 0);
@@ -610,7 +612,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           } else {
             const bool move = row_ok && mt > m + kTreeSlack;
             if (__any_sync(0xffffffffu, move)) {
-              // the stream's last product is complete before its sums are scaled
+              // the stream's last product is complete before its sums are scaled (the one before it is: these scores
+              // were issued after it)
               ok = __all_sync(0xffffffffu, tree_wait(&ms.o_done[st], (cnt - 1) & 1, a.status));
               if (ok) {
                 tc_fence_after();
@@ -650,10 +653,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
 
       // ---- the segment's sums ----
-      // the last two products may both be under way: one phase after the other
+      // a barrier of their own: of o_done's phases the last two may both be under way, or both over when a warp
+      // comes here late, and a parity does not tell these apart
       if (two || nt > st) {
-        if (ok && cnt > 1) ok = tree_wait(&ms.o_done[st], (cnt - 2) & 1, a.status);
-        if (ok) ok = tree_wait(&ms.o_done[st], (cnt - 1) & 1, a.status);
+        if (ok) ok = tree_wait(&ms.o_last[st], ends & 1, a.status);
+        ++ends;
       }
       ok = __all_sync(0xffffffffu, ok);
       float w0 = 1.f, w1 = 0.f;
@@ -803,6 +807,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int i = 0; i < kTreeKeys / 16; ++i)
                 mma_ts_lo(to, from + i * 8, vd + i * (2048 >> 4), kHalf, idO, i > 0 ? 1u : add);
               mma_commit(&ms.o_done[sk]);
+              if (k + (two ? 1 : 2) >= nt) mma_commit(&ms.o_last[sk]);
               mma_commit(&ms.empty[s]);
               if (!two) mma_commit(&ms.empty[s]);
             }
