@@ -477,9 +477,8 @@ orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const 
  * In every layer and KV head, scratch row path[j] of k_blk and v_blk
  * ([n_layers][batch][Hkv][blk_stride][d]) is copied to cache row len[b] + j
  * ([n_layers][batch][Hkv][capacity][d]), j = 0..a. Outputs and inputs must not overlap but for len and
- * new_len. Elements are
- * 16 bits wide, d a multiple of 8, the four buffers 16-byte aligned. A sequence without
- * room (len + a + 1 > capacity: status ORTHRUS_ERR_CAPACITY), an idle one (n_nodes[b] = 0), or any
+ * new_len. Elements are 16 bits wide, d a multiple of 8, the four buffers 16-byte aligned. A sequence
+ * without room (len + a + 1 > capacity: status ORTHRUS_ERR_CAPACITY), an idle one (n_nodes[b] = 0), or any
  * while the status word holds an error commits nothing: accept_len = -1, path and committed all -1,
  * pending and the cache unchanged, new_len = len. Errors: ORTHRUS_ERR_ARG, ORTHRUS_ERR_UNSUPPORTED, ORTHRUS_ERR_CUDA. */
 orthrus_status orthrus_tree_commit(const int32_t* parents, const int32_t* tokens, const int32_t* argmax,

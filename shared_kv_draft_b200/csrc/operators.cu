@@ -30,7 +30,7 @@ orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap
     return ORTHRUS_ERR_CUDA;
   // no unit is cut where units and keys are few enough for the even division with one part a unit
   const int units = a.B * a.Hkv * ((a.N * a.G + kTreeRows - 1) / kTreeRows);
-  const int tiles = (a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
+  const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
   if (units <= sms && tiles <= kTreeMinTiles && kTreeUnit + tiles * kTreeCost2 <= kTreeSwitch + kTreeUnit + kTreeCost1)
     return ORTHRUS_OK;
   const dim3 grid(std::min(sms - 1, units), (std::min(kTreeRows, a.N * a.G) + 31) / 32);

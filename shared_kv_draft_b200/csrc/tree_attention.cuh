@@ -10,8 +10,12 @@
 // the two products (4 x 256 x d flops a key) need as long as the reads, and the exponentials,
 // 16 a cycle and SM, four fifths of that. Measured at d = 128: 128 rows or fewer 5.4 TB/s over
 // a long cache (8 sequences of 16384 keys, 16 nodes x 4: 99 us, 83% of the copy rate); 256 rows
-// 3.7 TB/s and 0.93 PFLOP/s (4 of 32768 keys, 64 x 4: 147 us). Short caches are bound by latency:
-// launch, first loads, two or three tiles, and the second kernel.
+// 3.7 TB/s and 0.93 PFLOP/s (4 of 32768 keys, 64 x 4: 147 us). There the loads alone take 100 us, the
+// products with the loads 124, the softmax with the loads 120: q and K come to the first product from shared
+// memory, 6 KB for 48 cycles of it, and the loads write there meanwhile. Short caches are bound by latency:
+// launch, first loads, two or three tiles, and the second kernel (1 sequence of 1024 keys: 12.4 us).
+//   Kept at 8 softmax warps of 64 keys a thread: 16 warps of 32 keys, which have to agree on the reference, took
+// 174 us there; S in one buffer and P in two beside it, so that the next scores come sooner, 152.
 //
 // Split. A unit is (sequence, KV head, group of up to 256 rows); its keys come in tiles of 64, cache
 // tiles first, then the tree's. The grid is a CTA an SM, and the lengths are on the device only,
@@ -81,13 +85,13 @@ static_assert(sizeof(TreeMisc) <= 2048, "misc area");
 // ---- who works on what ------------------------------------------------------------------
 
 // Relative times, in steps of about 0.4 us. A tile took 0.78 us with up to 128 rows (bound by its reads) and
-// 1.06 us with 256; 3 : 4 instead of 2 : 3 cost 7% at 16 ragged sequences. What a unit costs beside its tiles
-// (pipeline filled and drained, sums stored) is about 3 us: 4 cost 6% there, 6 2%, 10 nothing.
+// 1.06 us with 256; 3 : 4 instead of 2 : 3 cost 10% at 16 ragged sequences. What a unit costs beside its tiles
+// (pipeline filled and drained, sums stored) is about 3 us; 6 or 10 instead of 8 cost nothing there.
 constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile with up to 128 rows, with more
 constexpr int kTreeUnit = 8;                   // a unit
 constexpr int kTreeSwitch = 10;                // how much longer than a range the even division's parts may be
 // Tiles of a part at least, in the even division: more parts are quicker to compute and slower to join. One
-// sequence of 1024 keys: 12.8 us with 2, 13.4 with 3, 13.8 with 4; a tree step of 100 keys 10.2, 8.5, 8.4.
+// sequence of 1024 keys: 12.6 us with 2 or 3, 12.9 with 4; a tree step of 100 keys 9.5, 7.9, 7.8.
 constexpr int kTreeMinTiles = 3;
 
 struct TreeSeq {
@@ -334,6 +338,26 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
+}
+
+// Two fp32 values in one register pair: one instruction for both (1% off the short caches, half of one elsewhere).
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
@@ -632,18 +656,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           }
           const float shift = m == -INFINITY ? 0.f : m - kTreeShift;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = pair2(sl, sl), shift2 = pair2(-shift, -shift);
+          uint64_t sum[2] = {0ull, 0ull};
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float p0 = fast_exp2(fmaf(v[2 * i], sl, -shift));
-            const float p1 = fast_exp2(fmaf(v[2 * i + 1], sl, -shift));
-            sum[(2 * i) & 3] += p0;
-            sum[(2 * i + 1) & 3] += p1;
+            float p0, p1;
+            unpair2(fma2(pair2(v[2 * i], v[2 * i + 1]), scale2, shift2), p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            sum[i & 1] = add2(sum[i & 1], pair2(p0, p1));
             pk[i] = tree_pack<BF16>(p0, p1);
           }
           tmem_put32(tS + buf * 64, pk);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float s0, s1;
+          unpair2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
           tmem_wait_st();
         }
         tc_fence_before();
