@@ -508,6 +508,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int i = 0; i < 8; ++i) ms.bad[i] = 0u;
     fence_barrier_init();
   }
+  // rows of q's tiles past the largest unit's last piece: zero, so that their scores, and the weights that nobody
+  // writes over them, are zero too: products of zeros take less power, which is what a long run has too little of
+  {
+    const int rows = min(kTreeRows, a.N * a.G), r0 = (rows + 31) / 32 * 32, r1 = rows > 128 ? kTreeRows : 128;
+    for (int i = threadIdx.x; i < (r1 - r0) * (D / 8); i += kTreeThreads) {
+      const int q = i / (D / 8), c = i - q * (D / 8), row = r0 + q;
+      *reinterpret_cast<uint4*>(sQ + (row >> 7) * S::kQTile + (c >> 3) * kQHalf + (row & 127) * 128 + (c & 7) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
   if (warp == kTreeMmaWarp) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
@@ -655,7 +666,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
             }
           }
-          const float shift = m == -INFINITY ? 0.f : m - kTreeShift;
+          const float shift = !row_ok ? INFINITY : m == -INFINITY ? 0.f : m - kTreeShift;  // no row: weights of zero
           const uint64_t scale2 = pair2(sl, sl), shift2 = pair2(-shift, -shift);
           uint64_t sum[2] = {0ull, 0ull};
           uint32_t pk[32];
