@@ -121,7 +121,7 @@ struct FwdArgs {
   int L, D, H, Hkv, d, F, V, G, qk_norm, mask_id;
   float eps, scale_log2;
   double theta;
-  int view;                  // VIEW_DRAFT / VIEW_VERIFY
+  int view;                  // VIEW_DRAFT / VIEW_VERIFY / VIEW_TREE (frozen weights, K/V to the scratch, masked block)
   int nb, Q, M, Mt, mt_idx, stages, cap, max_block, batch;
   int lookahead;             // weight tiles the weight producer loads ahead of a phase's input dependency
   int poll_ns;               // sleep between polls of a phase counter
@@ -129,7 +129,9 @@ struct FwdArgs {
                              // so a row's softmax runs over the same absolute key chunks whatever
                              // the block size: verify rows equal the plain AR rows bit for bit
   const int* pending;        // [nb]
-  const int* draft_ids;      // verify: [nb][Q-1]; draft: nullable [nb][Q], the previous drafts
+  const int* draft_ids;      // verify: [nb][Q-1]; draft: nullable [nb][Q], the previous drafts; tree: [nb][Q]
+  const int *tree_depth, *n_nodes;      // tree: [nb][Q]; [nb], nullable
+  const unsigned long long* tree_mask;  // tree: [nb][Q][(Q + 63) / 64]
   int* len;                  // [batch] (read; the fused accept advances it)
   const __nv_bfloat16* embed;
   const float* final_norm;
@@ -317,7 +319,7 @@ __device__ inline int slot_visible_keys(const FwdArgs& a, const FwdGeom& g, cons
   const int r = s % g.rt;
   const int bb = s / (g.rt * a.Hkv);
   const int n = min(lens[bb], a.cap);
-  if (a.view == VIEW_DRAFT) return n;  // cache keys; the block is one extra chunk
+  if (a.view != VIEW_VERIFY) return n;  // cache keys; the block is one extra chunk
   const int row_hi = min(g.rows_per_slot, (r + 1) * 128);
   const int i_max = (row_hi - 1) / a.G;
   return min(n + i_max + 1, a.cap);
@@ -326,7 +328,7 @@ __device__ inline int slot_visible_keys(const FwdArgs& a, const FwdGeom& g, cons
 __device__ inline int slot_chunks(const FwdArgs& a, const FwdGeom& g, const int* lens, int s) {
   const int vis = slot_visible_keys(a, g, lens, s);
   const int c = (vis + g.CK - 1) / g.CK;
-  return a.view == VIEW_DRAFT ? c + 1 : max(1, c);
+  return a.view != VIEW_VERIFY ? c + 1 : max(1, c);
 }
 
 }  // namespace orthrus
@@ -354,7 +356,7 @@ __device__ inline AttUnit att_unit(const FwdArgs& a, const FwdGeom& g, const int
   t.bb = lo / (g.rt * a.Hkv);
   t.n = min(lens[t.bb], a.cap);
   const int vis = slot_visible_keys(a, g, lens, lo);
-  if (a.view == VIEW_DRAFT && t.chunk == t.n_chunks - 1) {
+  if (a.view != VIEW_VERIFY && t.chunk == t.n_chunks - 1) {
     t.blk = 1;
     t.key_lo = 0;
     t.key_hi = a.Q;
@@ -570,7 +572,7 @@ __device__ __forceinline__ void qkv_item(const FwdArgs& a, const QkvCtx& q, cons
       dst = a.qbuf + ((size_t)(bb * a.Hkv + kvh) * (a.Q * G) + i * G + g) * d;
     } else {
       const int kvh = hh - a.H - (kind == 2 ? a.Hkv : 0);
-      const int slot = a.view == VIEW_DRAFT ? i : lens_s[bb] + i;
+      const int slot = a.view != VIEW_VERIFY ? i : lens_s[bb] + i;
       if (slot >= 0 && slot < q.kv_stride)
         dst = (kind == 1 ? q.kdst : q.vdst) + ((size_t)(bb * a.Hkv + kvh) * q.kv_stride + slot) * d;
 #pragma unroll
@@ -589,7 +591,7 @@ __device__ __forceinline__ void qkv_item(const FwdArgs& a, const QkvCtx& q, cons
 // q/k/v epilogue on token rows [m0, m0+32) (+ the second group v2) of one 128-row tile (one
 // head at d = 128, two at d = 64): per-head RMSNorm of q and k, rotate-half RoPE at the row's
 // absolute position, bf16 store of q (qbuf) and of k, v (cache slot len+i in the verify view,
-// block-scratch row i in the draft view). Thread = (token row j, quarter qq): d/32 threads per
+// block-scratch row i in the others). Thread = (token row j, quarter qq): d/32 threads per
 // head, each holding elements [16s, 16s+16) and their RoPE partners [d/2 + 16s, d/2 + 16s + 16).
 // The second group's (row, quarter) items run on the first warp.
 template <int D_HEAD>
@@ -898,7 +900,9 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
       for (int m = c; m < a.M; m += Gd) {
         const int bb = m / a.Q, i = m - bb * a.Q;
         int id;
-        if (i == 0) id = a.pending[bb];
+        if (a.view == VIEW_TREE && a.n_nodes && i >= a.n_nodes[bb]) id = 0;  // padding
+        else if (i == 0) id = a.pending[bb];
+        else if (a.view == VIEW_TREE) id = a.draft_ids[m];
         else if (a.view == VIEW_VERIFY) id = a.draft_ids[bb * (a.Q - 1) + i - 1];
         else id = a.draft_ids ? a.draft_ids[bb * a.Q + i - 1] : a.mask_id;  // refinement: previous drafts
         if (id < 0 || id >= a.V) {
@@ -922,7 +926,7 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
         named_bar_sync(1, 128);
         if (et < parts) a.ss[(size_t)et * a.ss_ld + m] = ((epi[et] + epi[64 + et]) + epi[128 + et]) + epi[192 + et];
         if (et < d / 2) {
-          const double ang = (double)(n + i) * pow(a.theta, -2.0 * (double)et / (double)d);
+          const double ang = (double)(n + (a.view == VIEW_TREE ? a.tree_depth[m] : i)) * pow(a.theta, -2.0 * (double)et / (double)d);
           a.rope[(size_t)m * (d / 2) + et] = make_float2((float)cos(ang), (float)sin(ang));
         }
         if (et == 0) a.amax[m] = 0ull;
@@ -988,7 +992,7 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
         }
         qc.rope_rows = min(a.M, (stg_floats - 2 * d) / d);
         if (l > 0) stage_rope();
-        if (dv) {
+        if (a.view != VIEW_VERIFY) {
           const size_t lo = (size_t)l * a.batch * a.Hkv * a.max_block * d;
           qc.kdst = a.blk_k + lo;
           qc.vdst = a.blk_v + lo;
@@ -1315,12 +1319,26 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
           if (et == 0) tl_mark<TL>(a, n_ph, p, j == 0 ? TL_R0 : TL_S_ACC);  // score tile ready
           tc_fence_after();
           const int key0 = t.key_lo + j * 64;
-          const int nv = min(max(lim - key0, 0), 64);  // keys of this tile the row sees
+          int nv = min(max(lim - key0, 0), 64);  // keys of this tile the row sees
           // Row maximum over the visible scores: two 32-column loads, four independent
           // chains (the scale is positive, so max(s) * scale = max(s * scale) exactly).
           // The scores are loaded again for the exponentials below rather than held:
           // fewer live registers leave room for independent work in both passes.
           float sv[32];
+          if (a.view == VIEW_TREE && t.blk) {
+            // nodes that the row does not see: -inf in place of the score; a row that sees none has no keys here
+            const unsigned long long see =
+                row_ok ? a.tree_mask[((size_t)t.bb * a.Q + i) * ((a.Q + 63) / 64) + (key0 >> 6)] : 0ull;
+#pragma unroll
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+              tmem_ld32(tSb + lane_base + c0, sv);
+              const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+              for (int tt = 0; tt < 32; ++tt) sv[tt] = (bits >> tt & 1u) ? sv[tt] : -INFINITY;
+              tmem_st32(tSb + lane_base + c0, sv);
+            }
+            if (see == 0ull) nv = 0;
+          }
           float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
           for (int c0 = 0; c0 < 64; c0 += 32) {
@@ -1587,10 +1605,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) forward_kernel(const __grid_co
     g.rt = (g.rows_per_slot + 127) / 128;
     g.slots = a.nb * a.Hkv * g.rt;
     g.CK = a.ck;
-    if (a.view == VIEW_DRAFT) {
+    if (a.view != VIEW_VERIFY) {
       // The verify view keeps the plan's chunk length, so that its rows and plain decoding
-      // see the same chunk boundaries. The draft view's rows are matched with no other
-      // launch, so its chunks are the shortest whose units (one per chunk, plus the block)
+      // see the same chunk boundaries. The others' rows are matched with no other
+      // launch, so their chunks are the shortest whose units (one per chunk, plus the block)
       // fit one wave of CTAs for the current cache lengths: lane j tries ck0 + 64 j.
       int n_max = 0;
       for (int bb = lane; bb < a.nb; bb += 32) n_max = max(n_max, min(lens_s[bb], a.cap));

@@ -31,7 +31,7 @@
 namespace orthrus {
 
 enum EpiKind : int { EPI_STORE = 0, EPI_RESID = 1, EPI_QKV = 2, EPI_SWIGLU = 3, EPI_ARGMAX = 4 };
-enum ViewMode : int { VIEW_DRAFT = 0, VIEW_VERIFY = 1 };
+enum ViewMode : int { VIEW_DRAFT = 0, VIEW_VERIFY = 1, VIEW_TREE = 2 };
 
 constexpr int kGemmThreads = 192;
 constexpr int kEpiStride = 132;  // padded row of the epilogue staging tile (floats)

@@ -313,9 +313,14 @@ cudaError_t launch_forward_d(cudaLaunchConfig_t& cfg, const FwdArgs& a, bool tl,
   return g2 ? launch_forward_inst<D, false, true>(cfg, a) : launch_forward_inst<D, false, false>(cfg, a);
 }
 
+// A draft tree's forward: the block's tokens, and its layout in the workspace.
+struct TreeBlock {
+  const int *tokens, *n_nodes;
+};
+
 orthrus_status launch_forward(const Plan* P, int view, int Q, const int* pending, const int* draft, int* out_ids,
                               float* logits, bool accept, int K, int* pending_out, int* accept_len, int* committed,
-                              cudaStream_t st) {
+                              cudaStream_t st, const TreeBlock* tree = nullptr) {
   const orthrus_config& c = P->cfg;
   FwdArgs a;
   memset(&a, 0, sizeof(a));
@@ -355,7 +360,12 @@ orthrus_status launch_forward(const Plan* P, int view, int Q, const int* pending
   a.lookahead = 2;  // k-pair tiles of run-ahead past an unmet dependency: 2 measured best
   a.poll_ns = 64;   // sleep between polls of a phase counter
   a.pending = pending;
-  a.draft_ids = draft;
+  a.draft_ids = tree ? tree->tokens : draft;
+  if (tree) {
+    a.n_nodes = tree->n_nodes;
+    a.tree_depth = P->tree_depth;
+    a.tree_mask = P->tree_mask;
+  }
   a.len = P->len;
   a.embed = (const __nv_bfloat16*)P->embed;
   a.final_norm = P->final_norm;
@@ -412,11 +422,6 @@ orthrus_status launch_forward(const Plan* P, int view, int Q, const int* pending
   else e = launch_forward_d<64>(cfg, a, a.tl != nullptr, g2);
   return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
 }
-
-// A draft tree's forward: the block's tokens, and its layout in the workspace.
-struct TreeBlock {
-  const int *tokens, *n_nodes;
-};
 
 // One forward over a block of Q rows for sequences [b0, b0+nb).
 //   kind: BLOCK_DRAFT / BLOCK_VERIFY / BLOCK_PREFILL
@@ -1329,7 +1334,12 @@ orthrus_status orthrus_verify_tree(const void* plan, const int32_t* pending, con
   orthrus_status s = launch_tree_layout(parents, n_nodes, P->B, nodes, P->tree_depth, P->tree_mask, P->status, st);
   if (s != ORTHRUS_OK) return s;
   const TreeBlock tree = {tokens, n_nodes};
-  s = forward(P, BLOCK_VERIFY, 0, P->B, nodes, pending, nullptr, nullptr, 0, 0, true, false, argmax, logits, st, &tree);
+  if (persistent_ok(P, nodes)) {
+    mark(P, ORTHRUS_KIND_FORWARD, st);
+    s = launch_forward(P, VIEW_TREE, nodes, pending, nullptr, argmax, logits, false, 0, nullptr, nullptr, nullptr, st, &tree);
+  } else {
+    s = forward(P, BLOCK_VERIFY, 0, P->B, nodes, pending, nullptr, nullptr, 0, 0, true, false, argmax, logits, st, &tree);
+  }
   mark(P, ORTHRUS_KIND_END, st);
   return s;
 }

@@ -745,6 +745,35 @@ def test_plan_tree_chain_and_block_agree():
     assert float((results[0][2] - results[1][2]).abs().max()) <= 2 * LOGITS
 
 
+@pytest.mark.parametrize("P", [3, 200])
+@pytest.mark.parametrize("N", [1, 16, 33, 47, 64])
+def test_plan_tree_in_one_launch_and_in_many(N, P):
+    """Few rows run through the persistent kernel, more than 128 through the kernels of each step: the same tree
+    in a batch of one and in a batch of many, with two roots and padding, gives the same logits up to rounding."""
+    o, shape, cap = lib(), synth.TINY_QK, 320
+    w = synth.make_weights(shape, 91, 92, gain_std=0.1)
+    prompt = synth.make_prompt(shape, P, 93)
+    parents, rng = random_parents(1, N, 94 + N, spread=12), np.random.default_rng(95)
+    if N > 12:
+        parents[0, 12] = -1
+    tokens, live = rng.integers(0, shape.vocab, (1, N)).astype(np.int32), max(1, N - 3)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, **CUDA)  # noqa: E731
+    got = []
+    for B in (1, 128 // N + 1):
+        dev = o.DeviceModel(shape, w, batch=B, capacity=cap, max_block=N, max_rows=max(256, B * (N + 1)))
+        pending, ar = z(B), z(B, N)
+        dev.prefill(torch.from_numpy(np.tile(prompt, (B, 1))).cuda(), [P] * B, pending)
+        logits = torch.zeros((B, N, shape.vocab), **CUDA)
+        dev.verify_tree(pending, i32(np.tile(tokens, (B, 1))), i32(np.tile(parents, (B, 1))), ar, n_nodes=i32([live] * B),
+                        logits=logits)
+        torch.cuda.synchronize()
+        assert dev.read_status() == 0 and dev.lens.tolist() == [P] * B
+        assert torch.equal(ar[:, :live].long(), logits[:, :live].argmax(-1))
+        assert float((logits[:, :live] - logits[:1, :live]).abs().max()) <= 2 * LOGITS
+        got.append((logits[0, :live].clone(), dev))
+    assert float((got[0][0] - got[1][0]).abs().max()) <= 2 * LOGITS
+
+
 def test_plan_tree_refusals():
     o, shape = lib(), synth.TINY
     w = synth.make_weights(shape, 81, 82)
