@@ -9,7 +9,7 @@
 // Bound: every key is read once for up to 256 rows (nodes x group) of a KV head: HBM. At 256 rows
 // the two products (4 x 256 x d flops a key) need as long as the reads, and the exponentials,
 // 16 a cycle and SM, four fifths of that. Measured at d = 128: 128 rows or fewer 5.8 TB/s over
-// a long cache (8 sequences of 16384 keys, 16 nodes x 4: 93 us, 89% of the copy rate); 256 rows
+// a long cache (8 sequences of 16384 keys, 16 nodes x 4: 89-93 us, 89% of the copy rate); 256 rows
 // 3.8 TB/s and 0.95 PFLOP/s (4 of 32768 keys, 64 x 4: 143 us, and 169 us in a run of a second, at the card's power
 // limit and 1.5 GHz). There the loads alone take 100 us, the
 // products with the loads 124, the softmax with the loads 120: q and K come to the first product from shared
