@@ -24,13 +24,16 @@ namespace {
 template <int D, bool BF16>
 orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap* m, cudaStream_t st) {
   if (!ensure_smem_attr(tree_attention_kernel<D, BF16>, TreeSmem<D>::kBytes)) return ORTHRUS_ERR_CUDA;
-  const int sms = num_sms();
+  const int units = a.B * a.Hkv * ((a.N * a.G + kTreeRows - 1) / kTreeRows);
+  const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
+  // a CTA an SM, but where the capacity shows that the even division has fewer parts, not many more than those (a
+  // quarter, since the parts are rounded down): the SMs left free can start the join early (1 sequence of 1024 keys:
+  // 11.4 us, with a CTA on every SM 12.4)
+  const int sms = (int)std::min<long long>(num_sms(), units * ((tiles + kTreeMinTiles - 1) / kTreeMinTiles) * 5 / 4);
   if (launch(tree_attention_kernel<D, BF16>, dim3(sms), dim3(kTreeThreads), TreeSmem<D>::kBytes, st, m[0], m[1], m[2],
              m[3], m[4], a) != cudaSuccess)
     return ORTHRUS_ERR_CUDA;
   // no unit is cut where units and keys are few enough for the even division with one part a unit
-  const int units = a.B * a.Hkv * ((a.N * a.G + kTreeRows - 1) / kTreeRows);
-  const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
   if (units <= sms && tiles <= kTreeMinTiles && kTreeUnit + tiles * kTreeCost2 <= kTreeSwitch + kTreeUnit + kTreeCost1)
     return ORTHRUS_OK;
   const dim3 grid(std::min(sms - 1, units), (std::min(kTreeRows, a.N * a.G) + 31) / 32);

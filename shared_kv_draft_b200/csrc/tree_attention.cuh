@@ -14,12 +14,12 @@
 // limit and 1.5 GHz). There the loads alone take 100 us, the
 // products with the loads 124, the softmax with the loads 120: q and K come to the first product from shared
 // memory, 6 KB for 48 cycles of it, and the loads write there meanwhile. Short caches are bound by latency:
-// launch, first loads, two or three tiles, and the second kernel (1 sequence of 1024 keys: 12.4 us).
+// launch, first loads, two or three tiles, and the second kernel (1 sequence of 1024 keys: 11.3 us).
 //   Kept at 8 softmax warps of 64 keys a thread: 16 warps of 32 keys, which have to agree on the reference, took
 // 174 us there; S in one buffer and P in two beside it, so that the next scores come sooner, 152.
 //
 // Split. A unit is (sequence, KV head, group of up to 256 rows); its keys come in tiles of 64, cache
-// tiles first, then the tree's. The grid is a CTA an SM, and the lengths are on the device only,
+// tiles first, then the tree's. The grid is a CTA an SM at most, and the lengths are on the device only,
 // so the CTAs divide the units by themselves (TreeShare below), by the tiles' costs: a ragged
 // batch loads every SM alike. A unit that one CTA has is finished there; of a unit that is cut,
 // each CTA stores its part (unnormalised sums, the reference and the weights' sum per row, fp32),
@@ -92,7 +92,7 @@ constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile with up to 128 rows, wi
 constexpr int kTreeUnit = 8;                   // a unit
 constexpr int kTreeSwitch = 10;                // how much longer than a range the even division's parts may be
 // Tiles of a part at least, in the even division: more parts are quicker to compute and slower to join. One
-// sequence of 1024 keys: 12.6 us with 2 or 3, 12.9 with 4; a tree step of 100 keys 9.5, 7.9, 7.8.
+// sequence of 1024 keys: 12.6 us with 2 or 3, 12.9 with 4 (with a CTA on every SM); a tree step of 100 keys 9.5, 7.9, 7.8.
 constexpr int kTreeMinTiles = 3;
 
 struct TreeSeq {
