@@ -810,6 +810,10 @@ __device__ inline void fwd_finalize(const FwdArgs& a, int n_ph) {
   }
   __syncthreads();
   for (int i = t; i < n_ph; i += blockDim.x) a.phase_cnt[i] = 0;
+  if (*(volatile int*)a.status != 0) {  // CTAs that gave up left their tiles' counts behind
+    const int tiles = max(max(a.V / 128, a.F / 64), max((a.H + 2 * a.Hkv) * a.d / 128, a.D / 128));
+    for (int i = t; i < tiles; i += blockDim.x) a.tile_cnt[i] = 0;
+  }
   if (t == 0) *a.exit_cnt = 0;
   __threadfence();
 }

@@ -796,6 +796,34 @@ def test_plan_tree_refusals():
         assert acc.tolist() == [-1] and dev.lens.tolist() == [6]
 
 
+def test_plan_goes_on_after_an_error():
+    """A tree whose parents are none stops the forward on its way; once the status is cleared, trees and
+    chains give the bits that they give without it."""
+    o, shape, N, P = lib(), synth.TINY_QK, 9, 40
+    w = synth.make_weights(shape, 96, 97, gain_std=0.1)
+    prompt = torch.from_numpy(synth.make_prompt(shape, P, 98)).view(1, P).cuda()
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, **CUDA)  # noqa: E731
+    tokens, parents = i32(np.arange(5, 5 + N)[None]), i32(random_parents(1, N, 99))
+    results = []
+    for bad in (0, 1, 5):
+        dev = o.DeviceModel(shape, w, batch=1, capacity=96, max_block=N, max_rows=64)
+        pending, ar, chain = z(1), z(1, N), z(1, N)
+        dev.prefill(prompt, [P], pending)
+        for _ in range(bad):
+            dev.verify_tree(pending, tokens, i32([[-1] + [7] * (N - 1)]), ar)
+            torch.cuda.synchronize()
+            assert dev.read_status() == o.ERR_ARG
+            dev.clear_status()
+        logits, more = torch.zeros((1, N, shape.vocab), **CUDA), torch.zeros((1, N, shape.vocab), **CUDA)
+        dev.verify_tree(pending, tokens, parents, ar, logits=logits)
+        dev.verify_block(pending, tokens[:, 1:].contiguous(), N - 1, chain, more)
+        torch.cuda.synchronize()
+        assert dev.read_status() == 0
+        results.append((logits, more))
+    for logits, more in results[1:]:
+        assert torch.equal(logits, results[0][0]) and torch.equal(more, results[0][1])
+
+
 def test_binding_refuses_what_does_not_fit():
     o = lib()
     a = make_attention(1, 2, 4, 9, 64, 128, [20], seed=1)
