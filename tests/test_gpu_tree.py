@@ -745,12 +745,16 @@ def test_plan_tree_chain_and_block_agree():
     assert float((results[0][2] - results[1][2]).abs().max()) <= 2 * LOGITS
 
 
+WIDE = synth.ModelShape("wide_heads", 2, 512, 8, 2, 128, 768, 1024, qk_norm=True)
+
+
+@pytest.mark.parametrize("shape", [synth.TINY_QK, WIDE], ids=["d64", "d128"])
 @pytest.mark.parametrize("P", [3, 200])
 @pytest.mark.parametrize("N", [1, 16, 33, 47, 64])
-def test_plan_tree_in_one_launch_and_in_many(N, P):
+def test_plan_tree_in_one_launch_and_in_many(N, P, shape):
     """Few rows run through the persistent kernel, more than 128 through the kernels of each step: the same tree
     in a batch of one and in a batch of many, with two roots and padding, gives the same logits up to rounding."""
-    o, shape, cap = lib(), synth.TINY_QK, 320
+    o, cap = lib(), 320
     w = synth.make_weights(shape, 91, 92, gain_std=0.1)
     prompt = synth.make_prompt(shape, P, 93)
     parents, rng = random_parents(1, N, 94 + N, spread=12), np.random.default_rng(95)
