@@ -490,12 +490,13 @@ orthrus_status orthrus_tree_commit(const int32_t* parents, const int32_t* tokens
 
 /* Verify view over a draft tree, with a plan: one forward of the frozen model over
  * [pending, tokens[b][1..nodes)] at positions len + depth, every node seeing the cache,
- * itself and its ancestors. tokens, parents, n_nodes as above; nodes <= max_block. Writes argmax (device int32 [batch][nodes])
- * and leaves the tree's base K/V in the block scratch, which the next draft or tree
+ * itself and its ancestors. tokens, parents, n_nodes as above; nodes <= max_block. Writes argmax (device int32
+ * [batch][nodes]) and leaves the tree's base K/V in the block scratch, which the next draft or tree
  * view overwrites; cache and len are not changed. logits (nullable): fp32
  * [batch][nodes][vocab]. Entries of padding nodes are unspecified. A tree that is a chain gives
  * what orthrus_verify_block gives, up to rounding. Errors: ORTHRUS_ERR_ARG; device status as
- * orthrus_verify_block and orthrus_tree_layout. */
+ * orthrus_verify_block and orthrus_tree_layout (outputs are then unspecified, and nothing is committed
+ * until the status is cleared). */
 orthrus_status orthrus_verify_tree(const void* plan, const int32_t* pending, const int32_t* tokens,
                                    const int32_t* parents, const int32_t* n_nodes, int32_t nodes, int32_t* argmax,
                                    float* logits, orthrus_stream stream);
