@@ -820,8 +820,10 @@ __device__ inline void fwd_finalize(const FwdArgs& a, int n_ph) {
 
 // Epilogue warps (2-5) of the persistent forward kernel. G2: the block has 33-36 token rows,
 // whose rows past 32 ride with the first epilogue call (a separate instantiation, so blocks of
-// at most 32 rows run without that code).
-template <int D_HEAD, bool TL, bool G2>
+// at most 32 rows run without that code). TREE: the tree view, likewise apart: with its masks and
+// positions behind a run-time test, the other views took 0.8% longer (verify of 33 rows at the Qwen3-8B shape
+// 4.40 ms, 4.36 apart; a draft block of 32 3.97 and 3.94).
+template <int D_HEAD, bool TL, bool G2, bool TREE>
 __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeom& g, uint8_t* smem,
                                                   uint32_t stage_bytes, int S, uint8_t* scr,
                                                   unsigned long long* red, float* rstd_s, const int* lens_s,
@@ -904,9 +906,9 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
       for (int m = c; m < a.M; m += Gd) {
         const int bb = m / a.Q, i = m - bb * a.Q;
         int id;
-        if (a.view == VIEW_TREE && a.n_nodes && i >= a.n_nodes[bb]) id = 0;  // padding
+        if (TREE && a.n_nodes && i >= a.n_nodes[bb]) id = 0;  // padding
         else if (i == 0) id = a.pending[bb];
-        else if (a.view == VIEW_TREE) id = a.draft_ids[m];
+        else if (TREE) id = a.draft_ids[m];
         else if (a.view == VIEW_VERIFY) id = a.draft_ids[bb * (a.Q - 1) + i - 1];
         else id = a.draft_ids ? a.draft_ids[bb * a.Q + i - 1] : a.mask_id;  // refinement: previous drafts
         if (id < 0 || id >= a.V) {
@@ -930,7 +932,8 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
         named_bar_sync(1, 128);
         if (et < parts) a.ss[(size_t)et * a.ss_ld + m] = ((epi[et] + epi[64 + et]) + epi[128 + et]) + epi[192 + et];
         if (et < d / 2) {
-          const double ang = (double)(n + (a.view == VIEW_TREE ? a.tree_depth[m] : i)) * pow(a.theta, -2.0 * (double)et / (double)d);
+          const int at = n + (TREE ? a.tree_depth[m] : i);
+          const double ang = (double)at * pow(a.theta, -2.0 * (double)et / (double)d);
           a.rope[(size_t)m * (d / 2) + et] = make_float2((float)cos(ang), (float)sin(ang));
         }
         if (et == 0) a.amax[m] = 0ull;
@@ -1329,7 +1332,7 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
           // The scores are loaded again for the exponentials below rather than held:
           // fewer live registers leave room for independent work in both passes.
           float sv[32];
-          if (a.view == VIEW_TREE && t.blk) {
+          if (TREE && t.blk) {
             // nodes that the row does not see: -inf in place of the score; a row that sees none has no keys here
             const unsigned long long see =
                 row_ok ? a.tree_mask[((size_t)t.bb * a.Q + i) * ((a.Q + 63) / 64) + (key0 >> 6)] : 0ull;
@@ -1545,7 +1548,7 @@ __device__ __forceinline__ void fwd_epilogue_role(const FwdArgs& a, const FwdGeo
 
 namespace orthrus {
 
-template <int D_HEAD, bool TL, bool G2>
+template <int D_HEAD, bool TL, bool G2, bool TREE>
 __global__ void __launch_bounds__(kFwdThreads, 1) forward_kernel(const __grid_constant__ FwdArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -1936,7 +1939,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) forward_kernel(const __grid_co
     }
   } else {
     // ======================= epilogue warps =======================
-    fwd_epilogue_role<D_HEAD, TL, G2>(a, g, smem, stage_bytes, S, scr, red, rstd_s, lens_s, slot_pre, ust_s, accf, acce, full,
+    fwd_epilogue_role<D_HEAD, TL, G2, TREE>(a, g, smem, stage_bytes, S, scr, red, rstd_s, lens_s, slot_pre, ust_s, accf, acce, full,
                               s_full, p_full, o_full, flag, tmem_base, tS, tO);
   }
 

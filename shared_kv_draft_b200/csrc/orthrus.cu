@@ -301,16 +301,16 @@ bool persistent_ok(const Plan* P, int Q) {
   return P->mega_slots > 0 && fwd_rows_fit(P->B * Q, P->cfg.head_dim) && Q <= P->max_block + 1;
 }
 
-template <int D, bool TL, bool G2>
+template <int D, bool TL, bool G2, bool TREE>
 cudaError_t launch_forward_inst(cudaLaunchConfig_t& cfg, const FwdArgs& a) {
-  if (!ensure_smem_attr(forward_kernel<D, TL, G2>, kSmemLimit)) return cudaErrorInvalidValue;
-  return cudaLaunchKernelEx(&cfg, forward_kernel<D, TL, G2>, a);
+  if (!ensure_smem_attr(forward_kernel<D, TL, G2, TREE>, kSmemLimit)) return cudaErrorInvalidValue;
+  return cudaLaunchKernelEx(&cfg, forward_kernel<D, TL, G2, TREE>, a);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_forward_d(cudaLaunchConfig_t& cfg, const FwdArgs& a, bool tl, bool g2) {
-  if (tl) return g2 ? launch_forward_inst<D, true, true>(cfg, a) : launch_forward_inst<D, true, false>(cfg, a);
-  return g2 ? launch_forward_inst<D, false, true>(cfg, a) : launch_forward_inst<D, false, false>(cfg, a);
+  if (tl) return g2 ? launch_forward_inst<D, true, true, TREE>(cfg, a) : launch_forward_inst<D, true, false, TREE>(cfg, a);
+  return g2 ? launch_forward_inst<D, false, true, TREE>(cfg, a) : launch_forward_inst<D, false, false, TREE>(cfg, a);
 }
 
 // A draft tree's forward: the block's tokens, and its layout in the workspace.
@@ -416,10 +416,11 @@ orthrus_status launch_forward(const Plan* P, int view, int Q, const int* pending
   cfg.numAttrs = 1;
   cudaError_t e;
   // the timeline instantiation only while a timeline buffer is set (profiling); the G2 one for
-  // blocks of 33-36 token rows (a K = 32 verify block)
+  // blocks of 33-36 token rows (a K = 32 verify block); the tree view's own for a draft tree
   const bool g2 = a.M > 32 && a.M <= 36;
-  if (c.head_dim == 128) e = launch_forward_d<128>(cfg, a, a.tl != nullptr, g2);
-  else e = launch_forward_d<64>(cfg, a, a.tl != nullptr, g2);
+  const bool timed = a.tl != nullptr;
+  if (c.head_dim == 128) e = tree ? launch_forward_d<128, true>(cfg, a, timed, g2) : launch_forward_d<128, false>(cfg, a, timed, g2);
+  else e = tree ? launch_forward_d<64, true>(cfg, a, timed, g2) : launch_forward_d<64, false>(cfg, a, timed, g2);
   return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_CUDA;
 }
 

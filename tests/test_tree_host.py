@@ -86,6 +86,16 @@ def test_plan_calls_refuse_a_null_plan(lib):
     assert lib.orthrus_accept_commit_tree(None, P, P, P, None, P, 4, P, P, P, None) == orthrus.ERR_ARG
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g2", [0, 1])
+def test_the_tree_view_has_kernels_of_its_own(lib, d, g2):
+    """The draft and verify views run without the tree view's masks: their kernel has no third view."""
+    with open(orthrus.LIB_PATH, "rb") as f:
+        built = f.read()
+    for tree in (0, 1):
+        assert f"orthrus14forward_kernelILi{d}ELb0ELb{g2}ELb{tree}EEE".encode() in built
+
+
 # ---- rotary ----------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kw", [
