@@ -48,7 +48,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "forward_kernel_traffic.json")
 # CUDA sources that hold no code of the persistent forward kernel (its traffic record stays valid
 # when only these change)
 NOT_FORWARD_SOURCES = {"sampling.cuh", "policy.cuh", "operators.cu", "operators.cuh", "rotary.cuh", "tree.cuh",
-                       "tree_attention.cuh"}
+                       "tree_attention.cuh", "tree_ring.cuh"}
 
 
 def kernel_sources_sha256():

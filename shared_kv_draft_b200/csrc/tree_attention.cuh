@@ -51,6 +51,7 @@
 #pragma once
 #include "operators.cuh"
 #include "ptx.cuh"
+#include "tree_ring.cuh"
 
 namespace orthrus {
 
@@ -363,10 +364,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
 
 __device__ __forceinline__ float max3(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
 
-// Ring positions of a segment's tiles: `ahead` tiles of K, then V and K in turn.
-__device__ __forceinline__ uint32_t tree_pos_k(int k, int ahead) { return k + max(0, k - ahead + 1); }
-__device__ __forceinline__ uint32_t tree_pos_v(int k, int ahead, int nt) { return k + min(nt, k + ahead); }
-
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // MMAs whose shared-memory descriptors are given by their low word (address >> 4 in bits 0-13, leading
@@ -534,7 +531,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const uint32_t tmem = ms.tmem;
 
   // of every role: segments, ring position of the segment (tiles go through the ring in the order of
-  // their use: `ahead` tiles of K, then V and K in turn), and whether no wait has run out
+  // their use: `ahead` tiles of K, then V and K in turn), and whether no wait has run out. After that both
+  // stand still; the load warp's are then the counts of the q and the tiles whose copies it has issued
   uint32_t seg = 0, base = 0;
   bool ok = true;
   // MMA warps: jobs of each stream so far, and the last segment's kind
@@ -786,7 +784,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int p = 0; p < 2 * nt; ++p) {
           if (p == lead) {
             const int pieces = (min(kTreeRows, g.live * a.G - g.rg * kTreeRows) + 31) / 32;  // of q, 32 rows each
-            if (seg > 0 && !(ok = tree_wait(&ms.q_empty, (seg - 1) & 1, a.status))) break;
+            if (seg > 0 && !(ok = tree_wait(&ms.q_empty, (seg - 1) & 1, a.status))) {
+              base += p;
+              break;
+            }
             // rows of the 128-row tiles past the last piece keep what they hold: no sum of another row sees them
             mbar_arrive_expect_tx(&ms.q_full, pieces * (S::kQTile / 4));
             const int qrow = z * a.N * a.G + g.rg * kTreeRows;
@@ -800,7 +801,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const bool val = p >= lead && (p >= 2 * nt - lead || ((p - lead) & 1) == 0);
           const int k = p < lead ? p : (p >= 2 * nt - lead ? p - nt : (p - lead) / 2 + (val ? 0 : lead));
           const uint32_t pos = base + p, s = pos % S::kStages, lap = pos / S::kStages;
-          if (!(ok = tree_wait(&ms.empty[s], (lap & 1) ^ 1u, a.status))) break;
+          if (!(ok = tree_wait(&ms.empty[s], (lap & 1) ^ 1u, a.status))) {
+            base += p;
+            seg += p >= lead ? 1 : 0;
+            break;
+          }
           mbar_arrive_expect_tx(&ms.full[s], S::kTile);
           const int t = g.t0 + k;
           const bool blk = t >= ct;
@@ -896,17 +901,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       if (last >= 0) note = make_int4(g.b, g.kvh, g.rg << 16 | min(kTreeRows, g.live * a.G - g.rg * kTreeRows), last);
     }
-    base += 2 * nt;
-    ++seg;
+    if (ok) {
+      base += 2 * nt;
+      ++seg;
+    }
   }
 
   if (warp == kTreeLoadWarp) {
-    // copies in flight land before the CTA ends: the last use of each stage
-    if (lane == 0 && seg > 0) {
-      tree_wait(&ms.q_full, (seg - 1) & 1, a.status);
+    // copies in flight land before the CTA ends: the last q and the last use of each stage, of what was issued
+    if (lane == 0) {
+      bool landed = seg == 0 || tree_wait(&ms.q_full, (seg - 1) & 1, a.status);
 #pragma unroll 1
-      for (uint32_t k = base > S::kStages ? base - S::kStages : 0; k < base; ++k)
-        tree_wait(&ms.full[k % S::kStages], (k / S::kStages) & 1, a.status);
+      for (uint32_t k = tree_pos_last(base, S::kStages); landed && k < base; ++k)
+        landed = tree_wait(&ms.full[k % S::kStages], (k / S::kStages) & 1, a.status);
     }
   } else if (warp >= kTreeMmaWarp && warp <= kTreeMmaWarp + 1) {
     if (issue) mma_commit(&ms.done[mine]);
