@@ -511,7 +511,7 @@ orthrus_status orthrus_accept_commit_tree(const void* plan, int32_t* pending, co
 /* ---- rotary positions --------------------------------------------------- */
 
 /* Frequencies of a rotary embedding: pair p turns by turns[p] full turns per position. Filled by
- * orthrus_rope_init; a caller with frequencies of its own may fill it directly. */
+ * orthrus_rope_init or orthrus_rope_init_from; a caller with frequencies of its own may fill it directly. */
 typedef struct {
   int32_t head_dim, rot_dim; /* dims [0, rot_dim) of a head are rotated, the others copied */
   int32_t interleaved;       /* pairs (2p, 2p + 1) if set, else (p, p + rot_dim / 2) */
@@ -537,6 +537,15 @@ enum { ORTHRUS_ROPE_NONE = 0, ORTHRUS_ROPE_LINEAR = 1, ORTHRUS_ROPE_BY_PARTS = 2
 orthrus_status orthrus_rope_init(orthrus_rope* rope, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
                                  float theta, int32_t scaling, float factor, int32_t original, float slow, float fast,
                                  float gain);
+
+/* The same with the numbers that the frequencies follow from in fp64, for those that fp32 does not hold: a factor of
+ * 1.3 rounded to fp32 turns a head by 0.03 rad too much at position 10^6. */
+typedef struct {
+  double theta, factor, slow, fast;
+} orthrus_rope_numbers;
+orthrus_status orthrus_rope_init_from(orthrus_rope* rope, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                      const orthrus_rope_numbers* numbers, int32_t scaling, int32_t original,
+                                      float gain);
 
 /* One tensor of an orthrus_rotary call: value (b, t, h, e) is read at
  *   src[b src_batch + t src_token + h src_head + e]     (strides in elements)

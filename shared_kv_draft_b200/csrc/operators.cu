@@ -213,43 +213,50 @@ orthrus_status orthrus_tree_commit(const int32_t* parents, const int32_t* tokens
 orthrus_status orthrus_rope_init(orthrus_rope* rope, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
                                  float theta, int32_t scaling, float factor, int32_t original, float slow, float fast,
                                  float gain) {
-  if (!rope || head_dim < 2 || head_dim > 2 * kRotaryMaxPairs || head_dim % 2 || rot_dim < 2 || rot_dim > head_dim ||
+  const orthrus_rope_numbers x = {theta, factor, slow, fast};
+  return orthrus_rope_init_from(rope, head_dim, rot_dim, interleaved, &x, scaling, original, gain);
+}
+
+orthrus_status orthrus_rope_init_from(orthrus_rope* rope, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                      const orthrus_rope_numbers* numbers, int32_t scaling, int32_t original,
+                                      float gain) {
+  if (!rope || !numbers || head_dim < 2 || head_dim > 2 * kRotaryMaxPairs || head_dim % 2 || rot_dim < 2 || rot_dim > head_dim ||
       rot_dim % 2)
     return ORTHRUS_ERR_ARG;
-  if (!(theta > 1.f && theta < INFINITY) || !(gain >= 0.f && gain < INFINITY) || scaling < ORTHRUS_ROPE_NONE ||
+  const double theta = numbers->theta, factor = numbers->factor, slow = numbers->slow, fast = numbers->fast;
+  if (!(theta > 1.0 && theta < INFINITY) || !(gain >= 0.f && gain < INFINITY) || scaling < ORTHRUS_ROPE_NONE ||
       scaling > ORTHRUS_ROPE_BY_INDEX)
     return ORTHRUS_ERR_ARG;
-  if (scaling != ORTHRUS_ROPE_NONE && !(factor >= 1.f && factor < INFINITY)) return ORTHRUS_ERR_ARG;
+  if (scaling != ORTHRUS_ROPE_NONE && !(factor >= 1.0 && factor < INFINITY)) return ORTHRUS_ERR_ARG;
   const bool ramp = scaling == ORTHRUS_ROPE_BY_PARTS || scaling == ORTHRUS_ROPE_BY_INDEX;
-  if (ramp && (original < 1 || !(slow > 0.f) || !(fast > slow) || !(fast < INFINITY))) return ORTHRUS_ERR_ARG;
+  if (ramp && (original < 1 || !(slow > 0.0) || !(fast > slow) || !(fast < INFINITY))) return ORTHRUS_ERR_ARG;
   const double two_pi = 6.283185307179586476925;
-  const double th = (double)theta, k = (double)factor;
   memset(rope, 0, sizeof(*rope));
   rope->head_dim = head_dim;
   rope->rot_dim = rot_dim;
   rope->interleaved = interleaved != 0;
-  rope->gain = gain > 0.f ? gain : (ramp ? (float)(0.1 * std::log(k) + 1.0) : 1.f);
+  rope->gain = gain > 0.f ? gain : (ramp ? (float)(0.1 * std::log(factor) + 1.0) : 1.f);
   double lo = 0, hi = 0;
   if (scaling == ORTHRUS_ROPE_BY_INDEX) {
     auto index = [&](double rotations) {
-      return rot_dim * std::log(original / (two_pi * rotations)) / (2.0 * std::log(th));
+      return rot_dim * std::log(original / (two_pi * rotations)) / (2.0 * std::log(theta));
     };
-    lo = std::max(std::floor(index((double)fast)), 0.0);
-    hi = std::min(std::ceil(index((double)slow)), (double)(rot_dim - 1));
+    lo = std::max(std::floor(index(fast)), 0.0);
+    hi = std::min(std::ceil(index(slow)), (double)(rot_dim - 1));
     hi = std::max(hi, lo + 1e-3);
   }
   for (int p = 0; p < rot_dim / 2; ++p) {
-    double f = std::pow(th, -2.0 * p / rot_dim);
+    double f = std::pow(theta, -2.0 * p / rot_dim);
     if (scaling == ORTHRUS_ROPE_LINEAR) {
-      f /= k;
+      f /= factor;
     } else if (ramp) {
       double keep;
       if (scaling == ORTHRUS_ROPE_BY_PARTS)
-        keep = (original * f / two_pi - (double)slow) / ((double)fast - (double)slow);
+        keep = (original * f / two_pi - slow) / (fast - slow);
       else
         keep = 1.0 - (p - lo) / (hi - lo);
       keep = std::min(std::max(keep, 0.0), 1.0);
-      f *= keep + (1.0 - keep) / k;
+      f *= keep + (1.0 - keep) / factor;
     }
     rope->turns[p] = f / two_pi;
   }

@@ -71,6 +71,10 @@ class Rope(C.Structure):
                 ("turns", C.c_double * 128)]
 
 
+class RopeNumbers(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("theta", "factor", "slow", "fast")]
+
+
 class RotaryPart(C.Structure):
     _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p)] + [
         (n, C.c_int32) for n in ("src_type", "dst_type", "heads", "group", "flags", "rows")] + [
@@ -121,6 +125,7 @@ SIGNATURES = [
     ("orthrus_verify_tree", _I32, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
     ("orthrus_accept_commit_tree", _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP]),
     ("orthrus_rope_init", _I32, [_VP, _I32, _I32, _I32, _F, _I32, _F, _I32, _F, _F, _F]),
+    ("orthrus_rope_init_from", _I32, [_VP, _I32, _I32, _I32, C.POINTER(RopeNumbers), _I32, _I32, _F]),
     ("orthrus_rotary", _I32, [_VP, _VP, _I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP]),
 ]
 
@@ -307,9 +312,10 @@ def rope(head_dim, rot_dim=None, theta=1.0e6, interleaved=False, scaling="none",
     r = Rope()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"rope: scaling must be one of {sorted(ROPE_SCALINGS)}")
-    _check("orthrus_rope_init",
-           load().orthrus_rope_init(C.byref(r), head_dim, head_dim if rot_dim is None else rot_dim, int(bool(interleaved)),
-                                    theta, ROPE_SCALINGS[scaling], factor, original, slow, fast, gain))
+    numbers = RopeNumbers(theta, factor, slow, fast)
+    _check("orthrus_rope_init_from",
+           load().orthrus_rope_init_from(C.byref(r), head_dim, head_dim if rot_dim is None else rot_dim,
+                                         int(bool(interleaved)), C.byref(numbers), ROPE_SCALINGS[scaling], original, gain))
     return r
 
 

@@ -148,6 +148,26 @@ def test_rope_table_is_the_formula(lib, scaling, rot, theta, factor, original, s
     assert not any(r.turns[rot // 2:])
 
 
+@pytest.mark.parametrize("scaling", ["none", "linear", "by_parts", "by_index"])
+@pytest.mark.parametrize("rot,theta,factor,original,slow,fast", [
+    (128, 17143.79, 1.3, 32768, 1.1, 31.7), (64, 500000.1, 2.7, 8191, 0.9, 3.3), (128, 1.0e6 + 0.1, 1.0 + 1e-9, 100, 0.1, 0.3)])
+def test_rope_table_of_parameters_that_fp32_does_not_hold(lib, scaling, rot, theta, factor, original, slow, fast):
+    """Rounded to fp32 first they would be off by up to 6e-8, which is 0.06 rad at position 10^6; each of the about
+    ten fp64 operations adds 2^-53, and the power's logarithm (below 14) multiplies by 28: 1e-14 in all."""
+    r = orthrus.rope(128, rot, theta, scaling=scaling, factor=factor, original=original, slow=slow, fast=fast)
+    turns, gain = formula(rot, theta, scaling, factor, original, slow, fast)
+    assert list(r.turns[:rot // 2]) == pytest.approx(turns, rel=1e-14)
+    assert r.gain == pytest.approx(gain, rel=2 ** -23)
+
+
+def test_rope_init_takes_the_same_numbers_in_fp32(lib):
+    r = orthrus.Rope()
+    assert lib.orthrus_rope_init(C.byref(r), 128, 64, 0, 5.0e5, 3, 8.0, 4096, 1.0, 32.0, 0.0) == orthrus.OK
+    assert bytes(r) == bytes(orthrus.rope(128, 64, 5.0e5, scaling="by_index", factor=8.0, original=4096))
+    assert lib.orthrus_rope_init(None, 128, 64, 0, 5.0e5, 0, 1.0, 1, 1.0, 32.0, 0.0) == orthrus.ERR_ARG
+    assert lib.orthrus_rope_init_from(C.byref(r), 128, 64, 0, None, 0, 1, 0.0) == orthrus.ERR_ARG
+
+
 def test_rope_gain_can_be_set(lib):
     assert orthrus.rope(64, scaling="by_parts", factor=4.0, original=100, gain=1.0).gain == 1.0
     assert orthrus.rope(64, gain=0.5).gain == 0.5
