@@ -305,18 +305,22 @@ def tree_commit(parents, tokens, argmax, k_blk, v_blk, k_cache, v_cache, len, ne
 
 
 @functools.lru_cache(maxsize=64)
+def _rope_table(head_dim, rot_dim, theta, interleaved, scaling, factor, original, slow, fast, gain) -> bytes:
+    r, numbers = Rope(), RopeNumbers(theta, factor, slow, fast)
+    _check("orthrus_rope_init_from",
+           load().orthrus_rope_init_from(C.byref(r), head_dim, rot_dim, interleaved, C.byref(numbers),
+                                         ROPE_SCALINGS[scaling], original, gain))
+    return bytes(r)
+
+
 def rope(head_dim, rot_dim=None, theta=1.0e6, interleaved=False, scaling="none", factor=1.0, original=1, slow=1.0,
          fast=32.0, gain=0.0) -> Rope:
-    """Frequencies of a rotary embedding (host only): the table for rotary(). The same arguments give the same
-    table object; it is not to be changed (fill a Rope for frequencies of one's own)."""
-    r = Rope()
+    """Frequencies of a rotary embedding (host only): the table for rotary(). Every call gives a table of its own,
+    which the caller may change."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"rope: scaling must be one of {sorted(ROPE_SCALINGS)}")
-    numbers = RopeNumbers(theta, factor, slow, fast)
-    _check("orthrus_rope_init_from",
-           load().orthrus_rope_init_from(C.byref(r), head_dim, head_dim if rot_dim is None else rot_dim,
-                                         int(bool(interleaved)), C.byref(numbers), ROPE_SCALINGS[scaling], original, gain))
-    return r
+    return Rope.from_buffer_copy(_rope_table(head_dim, head_dim if rot_dim is None else rot_dim, theta,
+                                             int(bool(interleaved)), scaling, factor, original, slow, fast, gain))
 
 
 def rotary(rope, parts, len=None, offsets=None, inverse=False, status=None, stream=None):

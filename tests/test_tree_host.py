@@ -173,6 +173,13 @@ def test_rope_gain_can_be_set(lib):
     assert orthrus.rope(64, gain=0.5).gain == 0.5
 
 
+def test_rope_tables_are_the_callers_own(lib):
+    r = orthrus.rope(64, theta=1.0e4)
+    want = bytes(r)
+    r.gain, r.turns[3], r.interleaved = 2.0, 7.0, 1
+    assert bytes(orthrus.rope(64, theta=1.0e4)) == want
+
+
 def rotary_part(**kw):
     a = dict(src=P, dst=P, src_type=orthrus.FP32, dst_type=orthrus.FP16, heads=4, group=1, flags=0, rows=0, src_batch=512,
              src_token=512, src_head=128, dst_batch=512, dst_token=512, dst_kv=128, dst_head=0)
