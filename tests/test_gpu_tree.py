@@ -397,6 +397,50 @@ def test_attention_offsets_past_32_bits():
     assert (got - acc / l).abs().max() <= 2.0 ** -11 * 3.0
 
 
+def test_attention_rows_past_32_bits_decide():
+    """One head of 16.9 million rows whose result comes from 128 of them: 64 past 2^31 bytes of K and V, 64 past 2^32,
+    their V values far apart. All other K and V are zero: a row that is skipped, or read from 2^31 or 2^32 bytes before
+    its place, moves the result, about 0.5, towards 2 or -1: by far more than the bound."""
+    n, N, G, d = 16_900_001, 3, 4, 128
+    a = make_attention(1, 1, G, N, d, 64, [0], seed=24, see=np.eye(N, dtype=bool)[None])
+    g = torch.Generator(device="cuda").manual_seed(25)
+    r = lambda *s: torch.randn(s, generator=g, **CUDA)  # noqa: E731
+    lo, hi = 2 ** 31 // (2 * d), 2 ** 32 // (2 * d)
+    far = torch.cat([torch.arange(lo, lo + 32), torch.arange(hi - 32, hi), torch.arange(hi, hi + 32),
+                     torch.arange(n - 32, n)]).cuda()
+    q = 1.5 + 0.1 * r(1, 1, N * G, d)                       # scores of 1.5 x 1 x 128 / sqrt(128) = 17
+    keys, vals = 1.0 + 0.01 * r(128, d), 0.1 * r(128, d) + torch.where(torch.arange(128, **CUDA) < 64, 2.0, -1.0)[:, None]
+    a["q"], keys, vals = q.half(), keys.half(), vals.half()
+    a["k_cache"], a["v_cache"] = (torch.zeros((1, 1, n + 3, d), dtype=torch.float16, **CUDA) for _ in range(2))
+    a["k_cache"][0, 0, far], a["v_cache"][0, 0, far] = keys, vals
+    a["k_cache"][0, 0, n:], a["v_cache"][0, 0, n:] = math.nan, math.nan
+    a["len"] = i32([n])
+    out, status = call_attention(a)
+    assert int(status.item()) == 0
+    got = out.view(N, G, d).reshape(N * G, d).double()
+    kb, vb = (a[k][0, 0].double() for k in ("k_blk", "v_blk"))
+    qd, kd, vd = a["q"][0, 0].double(), keys.double(), vals.double()
+    node = torch.arange(N * G, **CUDA) // G
+    own = (qd * kb[node]).sum(1, keepdim=True) * d ** -0.5  # a node sees itself alone
+
+    def result(rows):
+        z = qd @ kd[rows].T * d ** -0.5
+        m = torch.maximum(z.amax(1, keepdim=True), own)
+        p, po = torch.exp(z - m), torch.exp(own - m)
+        total = p.sum(1, keepdim=True) + po + (n - rows.numel()) * torch.exp(-m)
+        return (p @ vd[rows] + po * vb[node]) / total, (p @ vd[rows].abs() + po * vb[node].abs()) / total
+
+    ref, spread = result(torch.arange(128, **CUDA))
+    mag = (qd.abs() @ kd.abs().T).amax() * d ** -0.5
+    rel = 2 * ((d + 4) * 2.0 ** -24 * mag + 2.0 ** -21 + (n / 128 + 160) * 2.0 ** -24) + HALF_STEP[torch.float16]
+    tol = rel * spread * 1.01 + HALF_STEP[torch.float16] * ref.abs() + 2.0 ** -24  # as in attention_bound
+    assert ((got - ref).abs() <= tol).all(), float(((got - ref).abs() / tol).max())
+    for part in (slice(0, 64), slice(64, 128)):  # what a kernel that misses either half would give
+        keep = torch.ones(128, dtype=torch.bool, **CUDA)
+        keep[part] = False
+        assert ((result(keep.nonzero()[:, 0])[0] - ref).abs() > 10 * tol).all()
+
+
 def test_attention_captured_and_on_two_streams():
     """A captured call replayed on new inputs; two calls at once on two streams, each with its scratch."""
     a, b = (make_attention(2, 2, 4, 33, 128, 1500, lens, seed=s) for lens, s in (([1400, 30], 17), ([0, 900], 18)))
