@@ -13,23 +13,42 @@ bool orthrus::tree_sizes_ok(int batch, int nodes) {
   return batch >= 1 && batch <= ORTHRUS_TREE_MAX_BATCH && nodes >= 1 && nodes <= ORTHRUS_TREE_MAX_NODES;
 }
 
+namespace {
+
 // Two parts for each CTA: of the unit in which its range starts, and of the one in which it ends.
-size_t orthrus::tree_attn_scratch(int B, int Hkv, int G, int nodes, int d) {
-  (void)B, (void)Hkv, (void)G, (void)nodes;
-  return (size_t)2 * num_sms() * kTreeRows * ((size_t)d * 4 + 8) + (size_t)num_sms() * sizeof(int4);
+size_t tree_part_bytes(int ctas, int d) {
+  return (size_t)2 * ctas * kTreeRows * ((size_t)d * 4 + 8) + (size_t)ctas * sizeof(int4);
+}
+
+long long tree_units(int B, int Hkv, int G, int nodes) {
+  return (long long)B * Hkv * (((long long)nodes * G + kTreeRows - 1) / kTreeRows);
+}
+
+long long tree_tiles(int nodes, int cap) {  // of a unit, at most
+  return ((long long)cap + kTreeKeys - 1) / kTreeKeys + (nodes + kTreeKeys - 1) / kTreeKeys;
+}
+
+// A CTA an SM, but where the capacity shows that the even division has fewer parts, not many more than those (a
+// quarter, since the parts are rounded down): the SMs left free can start the join early (1 sequence of 1024 keys in a
+// cache of that length: 11.3 us, with a CTA on every SM, as in a cache of 8192, 12.3)
+int tree_ctas(int B, int Hkv, int G, int nodes, int cap) {
+  const long long parts = (tree_tiles(nodes, cap) + kTreeMinTiles - 1) / kTreeMinTiles;
+  return (int)std::min<long long>(num_sms(), tree_units(B, Hkv, G, nodes) * parts * 5 / 4);
+}
+
+}  // namespace
+
+size_t orthrus::tree_attn_scratch(int B, int Hkv, int G, int nodes, int d, int cap) {
+  return tree_part_bytes(tree_ctas(B, Hkv, G, nodes, cap), d);
 }
 
 namespace {
 
 template <int D, bool BF16>
-orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap* m, cudaStream_t st) {
+orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap* m, int sms, cudaStream_t st) {
   if (!ensure_smem_attr(tree_attention_kernel<D, BF16>, TreeSmem<D>::kBytes)) return ORTHRUS_ERR_CUDA;
-  const int units = a.B * a.Hkv * ((a.N * a.G + kTreeRows - 1) / kTreeRows);
-  const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
-  // a CTA an SM, but where the capacity shows that the even division has fewer parts, not many more than those (a
-  // quarter, since the parts are rounded down): the SMs left free can start the join early (1 sequence of 1024 keys:
-  // 11.4 us, with a CTA on every SM 12.4)
-  const int sms = (int)std::min<long long>(num_sms(), units * ((tiles + kTreeMinTiles - 1) / kTreeMinTiles) * 5 / 4);
+  const int units = (int)tree_units(a.B, a.Hkv, a.G, a.N);
+  const long long tiles = tree_tiles(a.N, a.cap);
   if (launch(tree_attention_kernel<D, BF16>, dim3(sms), dim3(kTreeThreads), TreeSmem<D>::kBytes, st, m[0], m[1], m[2],
              m[3], m[4], a) != cudaSuccess)
     return ORTHRUS_ERR_CUDA;
@@ -46,16 +65,17 @@ orthrus_status launch_tree_attention_as(const TreeAttnArgs& a, const CUtensorMap
 
 }  // namespace
 
-orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* workspace, cudaStream_t st) {
+orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* workspace, size_t bytes, cudaStream_t st) {
   if (!encode_fn()) return ORTHRUS_ERR_CUDA;
   TreeAttnArgs a = args;
-  a.part_o = (float4*)workspace;
-  a.part_ml = (float2*)(a.part_o + (size_t)2 * num_sms() * kTreeRows * (a.d / 4));
-  a.note = (int4*)(a.part_ml + (size_t)2 * num_sms() * kTreeRows);
   // the costs of all tiles are counted in 31 bits
-  const long long tiles = ((long long)a.cap + kTreeKeys - 1) / kTreeKeys + (a.N + kTreeKeys - 1) / kTreeKeys;
-  const long long units = (long long)a.B * a.Hkv * (((long long)a.N * a.G + kTreeRows - 1) / kTreeRows);
-  if (units * (kTreeUnit + tiles * kTreeCost2) > INT32_MAX) return ORTHRUS_ERR_UNSUPPORTED;
+  if (tree_units(a.B, a.Hkv, a.G, a.N) * (kTreeUnit + tree_tiles(a.N, a.cap) * kTreeCost2) > INT32_MAX)
+    return ORTHRUS_ERR_UNSUPPORTED;
+  const int sms = tree_ctas(a.B, a.Hkv, a.G, a.N, a.cap);
+  if (bytes < tree_part_bytes(sms, a.d)) return ORTHRUS_ERR_WORKSPACE;
+  a.part_o = (float4*)workspace;
+  a.part_ml = (float2*)(a.part_o + (size_t)2 * sms * kTreeRows * (a.d / 4));
+  a.note = (int4*)(a.part_ml + (size_t)2 * sms * kTreeRows);
   const CUtensorMapDataType dt = a.bf16 ? kBF16 : kF16;
   const uint64_t z = (uint64_t)a.B * a.Hkv;
   CUtensorMap m[5];
@@ -66,8 +86,10 @@ orthrus_status orthrus::launch_tree_attention(const TreeAttnArgs& args, void* wo
                   map3d(&m[4], a.v_blk, a.d, a.blk_stride, z, kTreeKeys, 1, dt);
   if (!ok) return ORTHRUS_ERR_ARG;
   if (a.d == 128)
-    return a.bf16 ? launch_tree_attention_as<128, true>(a, m, st) : launch_tree_attention_as<128, false>(a, m, st);
-  return a.bf16 ? launch_tree_attention_as<64, true>(a, m, st) : launch_tree_attention_as<64, false>(a, m, st);
+    return a.bf16 ? launch_tree_attention_as<128, true>(a, m, sms, st)
+                  : launch_tree_attention_as<128, false>(a, m, sms, st);
+  return a.bf16 ? launch_tree_attention_as<64, true>(a, m, sms, st)
+                : launch_tree_attention_as<64, false>(a, m, sms, st);
 }
 
 orthrus_status orthrus::launch_tree_layout(const int* parents, const int* n_nodes, int batch, int nodes, int* depth,
@@ -121,7 +143,7 @@ size_t orthrus_tree_attention_workspace_bytes(int32_t batch, int32_t n_kv_heads,
                                               int32_t head_dim) {
   if (!tree_sizes_ok(batch, nodes) || n_kv_heads < 1 || group < 1 || group > 32 || (head_dim != 64 && head_dim != 128))
     return 0;
-  return tree_attn_scratch(batch, n_kv_heads, group, nodes, head_dim);
+  return tree_part_bytes(num_sms(), head_dim);  // for any capacity
 }
 
 orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const void* v_cache, const void* k_blk,
@@ -141,7 +163,7 @@ orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const 
   for (const void* p : {q, k_cache, v_cache, k_blk, v_blk, (const void*)out})
     if (!aligned(p, 16)) return ORTHRUS_ERR_ARG;
   if (!aligned(mask, 8) || !aligned(workspace, 256)) return ORTHRUS_ERR_ARG;
-  if (workspace_bytes < tree_attn_scratch(batch, n_kv_heads, group, nodes, head_dim)) return ORTHRUS_ERR_WORKSPACE;
+  if (workspace_bytes < tree_part_bytes(num_sms(), head_dim)) return ORTHRUS_ERR_WORKSPACE;
   TreeAttnArgs a;
   memset(&a, 0, sizeof(a));
   a.q = q;
@@ -166,7 +188,7 @@ orthrus_status orthrus_tree_attention(const void* q, const void* k_cache, const 
   a.out = out;
   a.out_lo = (size_t)batch * nodes * n_kv_heads * group * head_dim;
   a.status = status;
-  return launch_tree_attention(a, workspace, (cudaStream_t)stream);
+  return launch_tree_attention(a, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
 orthrus_status orthrus_tree_commit(const int32_t* parents, const int32_t* tokens, const int32_t* argmax,

@@ -35,9 +35,9 @@ struct TreeEmbedArgs {
 };
 
 bool tree_sizes_ok(int batch, int nodes);
-// Scratch of one tree attention call (bytes).
-size_t tree_attn_scratch(int B, int Hkv, int G, int nodes, int d);
-orthrus_status launch_tree_attention(const TreeAttnArgs& a, void* workspace, cudaStream_t st);
+// Scratch of one tree attention call over caches of `cap` rows (bytes); grows with each argument.
+size_t tree_attn_scratch(int B, int Hkv, int G, int nodes, int d, int cap);
+orthrus_status launch_tree_attention(const TreeAttnArgs& a, void* workspace, size_t bytes, cudaStream_t st);
 orthrus_status launch_tree_layout(const int* parents, const int* n_nodes, int batch, int nodes, int* depth,
                                   unsigned long long* mask, int* status, cudaStream_t st);
 orthrus_status launch_tree_embed(const TreeEmbedArgs& a, int rows, cudaStream_t st);

@@ -52,6 +52,7 @@ struct alignas(64) Plan {
   float* gemm_part;
   int* gemm_cnt;
   float* att_o;
+  size_t att_o_bytes;
   float2* att_ml;
   int* att_cnt;
   // persistent forward kernel
@@ -137,7 +138,7 @@ int attn_chunk_keys(int B, int Hkv, int row_tiles, int cap) {
 struct WsLayout {
   size_t status, h, xn, qbuf, attn, act, rope, amax, draft_ids, ar_ids, samp, samp_tot, gemm_part, gemm_cnt, att_o, att_ml, att_cnt,
       blk_k, blk_v, dev_maps, dev_norms, phase_cnt, ss, fwd_att_o, fwd_att_ml, tree_depth,
-      tree_mask, total;
+      tree_mask, att_o_bytes, total;
   int chunk_keys, attn_slots, ss_ld, mega_slots;
 };
 
@@ -204,8 +205,13 @@ WsLayout ws_layout(const orthrus_config* c, int B, int max_block, int max_rows_r
   w.samp_tot = take((size_t)B * max_block * kSampMaxTiles * 4);
   w.gemm_part = take((size_t)2 * sms * 128 * 128 * 4);
   w.gemm_cnt = take((size_t)gemm_counter_count(c, max_rows) * 4);
-  // the chunk partials of the per-op attention, or the scratch of the tree attention
-  w.att_o = take(std::max((size_t)w.attn_slots * 128 * d * 4, tree_attn_scratch(B, Hkv, G, max_block, d)));
+  // the chunk partials of the per-op attention, or, if some tree's block takes the per-op kernels, the scratch of the
+  // tree attention
+  w.mega_slots = mega_slots(c, B, max_block);
+  w.att_o_bytes = (size_t)w.attn_slots * 128 * d * 4;
+  if (w.mega_slots == 0 || !fwd_rows_fit(B * max_block, d))
+    w.att_o_bytes = std::max(w.att_o_bytes, tree_attn_scratch(B, Hkv, G, max_block, d, cap));
+  w.att_o = take(w.att_o_bytes);
   w.att_ml = take((size_t)w.attn_slots * 128 * 8);
   w.att_cnt = take((size_t)std::max(B * Hkv * rt_dec, Hkv * rt_pre) * 4);
   const size_t blk = (size_t)L * B * Hkv * max_block * d * 2;
@@ -216,7 +222,6 @@ WsLayout ws_layout(const orthrus_config* c, int B, int max_block, int max_rows_r
   w.phase_cnt = take((size_t)(fwd_n_phases(L) + 1) * 4);
   w.ss_ld = max_rows;
   w.ss = take((size_t)(D / 128) * max_rows * 4);
-  w.mega_slots = mega_slots(c, B, max_block);
   w.fwd_att_o = take((size_t)std::max(1, w.mega_slots) * kMaxChunks * 128 * d * 4);
   w.fwd_att_ml = take((size_t)std::max(1, w.mega_slots) * kMaxChunks * 128 * 8);
   w.tree_depth = take((size_t)B * max_block * 4);
@@ -574,7 +579,7 @@ orthrus_status forward(const Plan* P, int kind, int b0, int nb, int Q, const int
       ta.out = P->attn;
       ta.out_lo = P->attn_lo;
       ta.status = P->status;
-      const orthrus_status ts = launch_tree_attention(ta, P->att_o, st);
+      const orthrus_status ts = launch_tree_attention(ta, P->att_o, P->att_o_bytes, st);
       if (ts != ORTHRUS_OK) return ts;
     } else if ((launch_attention(d, P->gmap(G_Q), P->gmap(G_KC), P->gmap(G_VC), P->gmap(G_KB), P->gmap(G_VB), aa,
                                  st)) != cudaSuccess) {
@@ -725,6 +730,7 @@ orthrus_status orthrus_plan_init(void* plan, size_t plan_bytes, const orthrus_co
   P->gemm_part = (float*)(base + wl.gemm_part);
   P->gemm_cnt = (int*)(base + wl.gemm_cnt);
   P->att_o = (float*)(base + wl.att_o);
+  P->att_o_bytes = wl.att_o_bytes;
   P->att_ml = (float2*)(base + wl.att_ml);
   P->att_cnt = (int*)(base + wl.att_cnt);
   P->blk_k = (__half*)(base + wl.blk_k);

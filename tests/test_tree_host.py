@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import synth
 from shared_kv_draft_b200 import orthrus
 from shared_kv_draft_b200.build import build
 
@@ -94,6 +95,15 @@ def test_the_tree_view_has_kernels_of_its_own(lib, d, g2):
         built = f.read()
     for tree in (0, 1):
         assert f"orthrus14forward_kernelILi{d}ELb0ELb{g2}ELb{tree}EEE".encode() in built
+
+
+def test_plans_whose_trees_run_in_one_launch_hold_no_scratch_for_them(lib):
+    """Beside the block's depths and visibility words, a plan holds the tree attention's scratch only where a block takes
+    the per-op kernels."""
+    size = lambda shape, B, cap, K: orthrus.workspace_bytes(orthrus.make_config(shape), B, cap, K, B * (K + 1))  # noqa: E731
+    # a whole plan of one sequence of the tiny shape took 22.8 MB before there were trees, with the scratch 42.6 MB
+    assert size(synth.TINY, 1, 64, 4) < 23_000_000
+    assert size(synth.QWEN3_8B, 1, 64, 4) < 53_100_000
 
 
 # ---- rotary ----------------------------------------------------------------------------------------
