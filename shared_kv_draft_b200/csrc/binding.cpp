@@ -298,4 +298,11 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Checks and marshalli
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "built_for", ORTHRUS_BUILT_FOR)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

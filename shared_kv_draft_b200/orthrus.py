@@ -272,6 +272,10 @@ def _native():
     if _binding is None:
         load()
         from . import _binding as module  # fails loudly when it has not been built
+        from .build import _binding_tag
+        if module.built_for != _binding_tag():  # tensors are handed over in torch's own structures
+            raise ImportError(f"_binding.so was built for {module.built_for}, this is {_binding_tag()}: build it with "
+                              "`python -m shared_kv_draft_b200.build`")
         _binding = module
     return _binding
 
