@@ -128,11 +128,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         _run([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp"]
              + objs, verbose)
         os.replace(LIB + ".tmp", LIB)
-    if force or not binding_up_to_date():
-        try:
+    try:
+        if force or not binding_up_to_date():
             _build_binding(verbose)
-        except (RuntimeError, OSError) as e:
-            warnings.warn(f"liborthrus.so is built, its native binding is not: {e}")
+    except (RuntimeError, OSError, ImportError) as e:  # ImportError: no torch
+        warnings.warn(f"liborthrus.so is built, its native binding is not: {e}")
     return LIB
 
 

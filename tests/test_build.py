@@ -36,6 +36,16 @@ def test_the_library_stands_without_the_binding(monkeypatch):
     assert b.library_up_to_date()
 
 
+def test_the_library_stands_without_torch(monkeypatch):
+    def absent():
+        raise ImportError("no torch")
+
+    b.build()
+    monkeypatch.setattr(b, "_binding_tag", absent)
+    with pytest.warns(UserWarning, match="no torch"):
+        assert b.build() == b.LIB
+
+
 def test_a_failing_library_raises(monkeypatch):
     monkeypatch.setattr(b, "library_up_to_date", lambda: False)
     monkeypatch.setattr(b, "_compile", lambda *a: b._run(["g++", "no-such-file.cpp"], False))
