@@ -553,7 +553,8 @@ orthrus_status orthrus_rope_init_from(orthrus_rope* rope, int32_t head_dim, int3
  *   dst[b dst_batch + row dst_token + (h / group) dst_kv + (h % group) dst_head + e],
  * row = t, or len[b] + t with ORTHRUS_ROTARY_APPEND (only rows in [0, rows) are
  * written; others set the status ORTHRUS_ERR_CAPACITY). A source may be broadcast (stride 0), a destination
- * not. group = 1 for plain heads; G with
+ * not, and a source's heads are one stride apart: the grouped q layout and rows from len[b] on are destinations only.
+ * group = 1 for plain heads; G with
  * dst_kv = nodes*G*d, dst_token = G*d, dst_head = d is the attention's q layout. */
 typedef struct {
   const void* src;

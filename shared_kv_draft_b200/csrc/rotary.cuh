@@ -1,6 +1,7 @@
 // Rotary positions as an operator of its own: heads turned at explicit positions on their
-// way from a projection's output to the attention's q layout and the KV cache (or from
-// gradients of the turned heads back to gradients of the projection).
+// way from a projection's output to the attention's q layout and the KV cache, or, by the inverse, gradients
+// of the turned heads on the way to gradients of the projection. A source has one stride for all of its heads:
+// gradients that lie in the grouped q layout, or in cache rows, are brought to [batch][tokens][heads][d] first.
 //
 // Pair p of the first rot dims of a head, (x1, x2), at position t becomes
 //     gain * (x1 cos a - x2 sin a,  x2 cos a + x1 sin a),   a = t f_p;
