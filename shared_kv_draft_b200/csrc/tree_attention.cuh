@@ -6,15 +6,19 @@
 // in one pass over the keys with a running reference m per row; a row that sees nothing
 // gives zeros.
 //
-// Bound: every key is read once for up to 256 rows (nodes x group) of a KV head: HBM. At 256 rows
-// the two products (4 x 256 x d flops a key) need as long as the reads, and the exponentials,
-// 16 a cycle and SM, four fifths of that. Measured at d = 128: 128 rows or fewer 5.8 TB/s over
-// a long cache (8 sequences of 16384 keys, 16 nodes x 4: 89-93 us, 89% of the copy rate); 256 rows
-// 3.8 TB/s and 0.95 PFLOP/s (4 of 32768 keys, 64 x 4: 143 us, and 169 us in a run of a second, at the card's power
-// limit and 1.5 GHz). There the loads alone take 100 us, the
-// products with the loads 124, the softmax with the loads 120: q and K come to the first product from shared
-// memory, 6 KB for 48 cycles of it, and the loads write there meanwhile. Short caches are bound by latency:
-// launch, first loads, two or three tiles, and the second kernel (1 sequence of 1024 keys: 11.3 us).
+// Bound: every key is read once for up to 256 rows (nodes x group) of a KV head. A key costs an SM, in cycles at
+// 1965 MHz, 4 d / 22.5 for its bytes, 4 rows d / 5650 for the two products (the rates of a copy and of a large product
+// over 148 SMs) and rows / 16 for the exponentials: at d = 128 and 256 rows 23, 23 and 16, with 128 rows 23, 12 and 8:
+// HBM, with the products as long at 256 rows. At d = 64 and 256 rows 11, 12 and 16: the exponentials.
+// Measured at d = 128: 128 rows or fewer 5.8 TB/s over a long cache (8 sequences of 16384 keys, 16 nodes x 4: 92 us, 89%
+// of the copy rate; 112 us in a run of a second, at the card's power limit); 256 rows 3.7 TB/s and 0.94 PFLOP/s
+// (4 of 32768 keys, 64 x 4: 143-150 us, and 169-174 us in a run of a second, at 1.5 GHz). There the loads alone take
+// 100 us, the products with the loads 124, the softmax with the loads 120: q and K come to the first product from shared
+// memory, 6 KB for 32 cycles of arithmetic (48 at 128 bytes a cycle), and the loads write there meanwhile. Measured at
+// d = 64, 4 sequences of 32768 keys: 256 rows 120 us (the exponentials alone 58), 128 rows 80 us (the bytes alone 41): a
+// tile is half as large there and takes nearly as long; which part of its chain sets the pace has not been taken apart.
+// Short caches are bound by latency: launch, first loads, two or three tiles, and the second kernel (1 sequence of 1024
+// keys: 11.3 us, in a cache for 8192 12.3).
 //   Kept at 8 softmax warps of 64 keys a thread: 16 warps of 32 keys, which have to agree on the reference, took
 // 174 us there; S in one buffer and P in two beside it, so that the next scores come sooner, 152.
 //
@@ -87,8 +91,9 @@ static_assert(sizeof(TreeMisc) <= 2048, "misc area");
 // ---- who works on what ------------------------------------------------------------------
 
 // Relative times, in steps of about 0.4 us. A tile took 0.78 us with up to 128 rows (bound by its reads) and
-// 1.06 us with 256; 3 : 4 instead of 2 : 3 cost 10% at 16 ragged sequences. What a unit costs beside its tiles
-// (pipeline filled and drained, sums stored) is about 3 us; 6 or 10 instead of 8 cost nothing there.
+// 1.06 us with 256 (d = 64, 4 x 32768 keys: 0.72 and 1.08); 3 : 4 instead of 2 : 3 cost 10% at 16 ragged sequences. What
+// a unit costs beside its tiles (pipeline filled and drained, sums stored) is about 3 us; 6 or 10 instead of 8 cost
+// nothing there.
 constexpr int kTreeCost1 = 2, kTreeCost2 = 3;  // a tile with up to 128 rows, with more
 constexpr int kTreeUnit = 8;                   // a unit
 constexpr int kTreeSwitch = 10;                // how much longer than a range the even division's parts may be
